@@ -15,6 +15,7 @@ from ._lib import (  # noqa: F401
     IPC_HANDLE_BYTES,
     MoEBoundaryError,
     ROUTE_FAST_SIGMOID_BOUND,
+    STAGE_BALANCE,
     STAGE_COMBINE,
     STAGE_COMBINE_JOIN,
     STAGE_DISPATCH,
@@ -24,6 +25,7 @@ from ._lib import (  # noqa: F401
     STAGE_ROUTE,
     STAGE_ROUTE_NORM_QUANT,
     STAGE_ROUTER_LOGITS,
+    balance_workspace_size,
     device_status,
     dispatch_workspace_size,
     expert_combine,
@@ -40,9 +42,11 @@ from ._lib import (  # noqa: F401
     last_error,
     lib_path,
     load,
+    moe_balance_loss,
     moe_dispatch,
     moe_dispatch_noalloc,
     moe_route,
+    moe_route_backward,
     moe_route_check_fast_sigmoid,
     moe_route_norm_quant,
     norm_quant_nvfp4,

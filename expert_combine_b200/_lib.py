@@ -63,6 +63,7 @@ STAGE_ROUTE_NORM_QUANT = 5
 STAGE_DISPATCH = 6
 STAGE_ROUTER_LOGITS = 7
 STAGE_FINALIZE_AR = 8
+STAGE_BALANCE = 9
 FAR_MAX_WORLD = 8
 IPC_HANDLE_BYTES = 64
 
@@ -112,6 +113,8 @@ def load() -> ctypes.CDLL:
                                          P, P],
                 "moe_dispatch": [P, i32, i32, i32, i32, P, P, P, P, ctypes.c_size_t, P],
                 "moe_dispatch_noalloc": [P, i32, i32, i32, i32, P, P, P, P],
+                "moe_balance_loss": [P, P, P, i32, i32, i32, P, i32, f32, P, P, P, P, P, ctypes.c_size_t, P],
+                "moe_route_backward": [P, P, P, i32, i32, i32, P, P, f32, P, P, P, i32, P, P],
                 "router_logits": [P, i32, i32, P, i32, f32, P, P],
                 "router_weight_prepare": [P, i32, i32, P, P],
                 "moe_boundary_supported": [i32, i32, i32, i32, i32, i32],
@@ -133,6 +136,8 @@ def load() -> ctypes.CDLL:
                 fn.restype = ctypes.c_char_p if name == "mb_last_error" else ctypes.c_int
             lib.moe_dispatch_workspace_size.argtypes = [i32, i32, i32]
             lib.moe_dispatch_workspace_size.restype = ctypes.c_size_t
+            lib.moe_balance_workspace_size.argtypes = [i32, i32, i32]
+            lib.moe_balance_workspace_size.restype = ctypes.c_size_t
             lib.finalize_ar_workspace_size.argtypes = [i32, i32, i32]
             lib.finalize_ar_workspace_size.restype = ctypes.c_size_t
             _lib = lib
@@ -165,6 +170,29 @@ def _want(t: torch.Tensor, dtype: torch.dtype, name: str) -> None:
         raise ValueError(f"{name}: expected a CUDA tensor")
     if not t.is_contiguous():
         raise ValueError(f"{name}: expected a contiguous tensor")
+
+
+class _on:
+    """The tensors' device as the current one, for calls whose tensors may live on another."""
+
+    __slots__ = ("dev", "guard")
+
+    def __init__(self, fn: str, first: torch.Tensor, *rest: Optional[torch.Tensor]):
+        self.dev = first.device
+        for t in rest:
+            if t is not None and t.device != self.dev:
+                raise ValueError(f"{fn}: tensors on {self.dev} and {t.device}")
+
+    def __enter__(self):
+        self.guard = None
+        if self.dev.index != torch.cuda.current_device():
+            self.guard = torch.cuda.device(self.dev)
+            self.guard.__enter__()
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+        return False
 
 
 def supported(stage: int, T: int = 1, H: int = 16, E: int = 1, k: int = 1, tp: int = 1) -> bool:
@@ -451,6 +479,102 @@ def moe_dispatch_noalloc(topk_ids: torch.Tensor, num_experts: int, expert_begin:
            load().moe_dispatch_noalloc(_ptr(topk_ids), T, k, int(expert_begin), E, _ptr(expert_offsets),
                                        _ptr(row_idx), _ptr(row_token), _stream(stream)))
     return expert_offsets, row_idx, row_token
+
+
+# ---------------------------------------------------------------------------- training the router
+def balance_workspace_size(T: int, E: int, Q: int = 1) -> int:
+    """Bytes of device workspace moe_balance_loss needs (0 when the sizes are not supported)."""
+    return int(load().moe_balance_workspace_size(T, E, Q))
+
+
+def _router_batch(fn, logits, topk_ids, token_mask, seq_offsets):
+    """-> (T, E, k, Q) of a router batch, checked."""
+    _want(logits, torch.float32, "logits")
+    _want(topk_ids, torch.int32, "topk_ids")
+    _want(token_mask, torch.uint8, "token_mask")
+    T, E = logits.shape
+    Q = 1
+    if seq_offsets is not None:
+        _want(seq_offsets, torch.int32, "seq_offsets")
+        Q = seq_offsets.numel() - 1
+    if topk_ids.dim() != 2 or topk_ids.shape[0] != T or token_mask.numel() != T or Q < 1:
+        raise ValueError(f"{fn}: shape mismatch")
+    return T, E, topk_ids.shape[1], Q
+
+
+@_traced
+def moe_balance_loss(logits: torch.Tensor, topk_ids: torch.Tensor, token_mask: torch.Tensor, coeff: float,
+                     seq_offsets: Optional[torch.Tensor] = None, loss: Optional[torch.Tensor] = None,
+                     counts: Optional[torch.Tensor] = None, prob_sums: Optional[torch.Tensor] = None,
+                     seq_tokens: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None, stream=None):
+    """Balance loss of the router gate ->
+    (loss float32 [1], counts int32 [Q, E], prob_sums float32 [Q, E], seq_tokens int32 [Q]).
+
+    ``seq_offsets`` (int32 [Q + 1] on the device, ascending) cuts the tokens
+    into the sequences the loss is averaged over; without it the batch is one.
+    ``workspace`` is a uint8 CUDA tensor of at least ``balance_workspace_size``
+    bytes; when omitted, one is allocated here."""
+    fn = "moe_balance_loss"
+    T, E, k, Q = _router_batch(fn, logits, topk_ids, token_mask, seq_offsets)
+    dev = logits.device
+    if loss is None:
+        loss = torch.empty(1, dtype=torch.float32, device=dev)
+    if counts is None:
+        counts = torch.empty(Q, E, dtype=torch.int32, device=dev)
+    if prob_sums is None:
+        prob_sums = torch.empty(Q, E, dtype=torch.float32, device=dev)
+    if seq_tokens is None:
+        seq_tokens = torch.empty(Q, dtype=torch.int32, device=dev)
+    if workspace is None:
+        workspace = torch.empty(balance_workspace_size(T, E, Q), dtype=torch.uint8, device=dev)
+    for t, dt, name in ((loss, torch.float32, "loss"), (counts, torch.int32, "counts"),
+                        (prob_sums, torch.float32, "prob_sums"), (seq_tokens, torch.int32, "seq_tokens"),
+                        (workspace, torch.uint8, "workspace")):
+        _want(t, dt, name)
+    if loss.numel() != 1 or counts.shape != (Q, E) or prob_sums.shape != (Q, E) or seq_tokens.numel() != Q:
+        raise ValueError(f"{fn}: shape mismatch")
+    with _on(fn, logits, topk_ids, token_mask, seq_offsets, loss, counts, prob_sums, seq_tokens, workspace):
+        _check(fn, load().moe_balance_loss(_ptr(logits), _ptr(topk_ids), _ptr(token_mask), T, E, k, _ptr(seq_offsets),
+                                           Q, float(coeff), _ptr(loss), _ptr(counts), _ptr(prob_sums),
+                                           _ptr(seq_tokens), _ptr(workspace), workspace.numel(), _stream(stream)))
+    return loss, counts, prob_sums, seq_tokens
+
+
+@_traced
+def moe_route_backward(logits: torch.Tensor, topk_ids: torch.Tensor, token_mask: torch.Tensor,
+                       grad_weights: Optional[torch.Tensor] = None, grad_loss: Optional[torch.Tensor] = None,
+                       coeff: float = 0.0, counts: Optional[torch.Tensor] = None,
+                       seq_tokens: Optional[torch.Tensor] = None, seq_offsets: Optional[torch.Tensor] = None,
+                       grad_logits: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Gradient of the router's logits (float32 [T, E]) from ``grad_weights``
+    (of moe_route's weights, float32 [T, k]), from ``grad_loss`` (of
+    moe_balance_loss's loss, float32 [1]; with that call's coeff, counts,
+    seq_tokens and seq_offsets), or from both."""
+    fn = "moe_route_backward"
+    T, E, k, Q = _router_batch(fn, logits, topk_ids, token_mask, seq_offsets)
+    if grad_weights is not None:
+        _want(grad_weights, torch.float32, "grad_weights")
+        if grad_weights.shape != (T, k):
+            raise ValueError(f"{fn}: shape mismatch")
+    if grad_loss is not None:
+        if counts is None or seq_tokens is None:
+            raise ValueError(f"{fn}: grad_loss needs counts and seq_tokens")
+        _want(grad_loss, torch.float32, "grad_loss")
+        _want(counts, torch.int32, "counts")
+        _want(seq_tokens, torch.int32, "seq_tokens")
+        if grad_loss.numel() != 1 or counts.shape != (Q, E) or seq_tokens.numel() != Q:
+            raise ValueError(f"{fn}: shape mismatch")
+    if grad_logits is None:
+        grad_logits = torch.empty(T, E, dtype=torch.float32, device=logits.device)
+    _want(grad_logits, torch.float32, "grad_logits")
+    if grad_logits.shape != (T, E):
+        raise ValueError(f"{fn}: shape mismatch")
+    with _on(fn, logits, topk_ids, token_mask, grad_weights, grad_loss, counts, seq_tokens, seq_offsets, grad_logits):
+        _check(fn, load().moe_route_backward(_ptr(logits), _ptr(topk_ids), _ptr(token_mask), T, E, k,
+                                             _ptr(grad_weights), _ptr(grad_loss), float(coeff), _ptr(counts),
+                                             _ptr(seq_tokens), _ptr(seq_offsets), Q, _ptr(grad_logits),
+                                             _stream(stream)))
+    return grad_logits
 
 
 @_traced

@@ -84,6 +84,12 @@ int moe_boundary_supported(int stage, int T, int H, int E, int k, int tp) {
                     static_cast<int64_t>(T) * k <= INT32_MAX)
                        ? 1
                        : 0;
+        case MB_STAGE_BALANCE:
+            return (k >= 1 && k <= kMaxTopK && E >= k && E <= kMaxExperts && T <= (1 << 30) &&
+                    static_cast<int64_t>(T) * k <= INT32_MAX && tp >= 1 && tp <= (1 << 20) &&
+                    static_cast<int64_t>(tp) * E <= INT32_MAX)
+                       ? 1
+                       : 0;
         case MB_STAGE_FINALIZE_AR:
             return (H >= 16 && H % 16 == 0 && H <= kMaxHidden && k >= 1 && k <= kMaxTopK && tp >= 1 &&
                     tp <= kFarMaxWorld)
@@ -325,6 +331,67 @@ int moe_dispatch(const int32_t* topk_ids, int T, int k, int expert_begin, int E,
     return cuda_status(launch_dispatch(topk_ids, T, k, expert_begin, E, expert_offsets, row_idx, row_token,
                                        workspace, static_cast<cudaStream_t>(stream)),
                        fn);
+}
+
+// ------------------------------------------------------------------ training the router
+static int check_balance(const char* fn, int T, int E, int k, const int32_t* seq_offsets, int Q) {
+    if (T < 0 || E < 0 || k < 0 || Q < 0) return fail(MB_ERR_INVALID_ARG, "%s: negative size", fn);
+    if (!moe_boundary_supported(MB_STAGE_BALANCE, T, 0, E, k, Q))
+        return fail(MB_ERR_UNSUPPORTED,
+                    "%s: needs 1 <= k <= %d, k <= E <= %d, T * k < 2^31, T <= 2^30, 1 <= Q <= 2^20 and Q * E < 2^31 "
+                    "(T=%d, k=%d, E=%d, Q=%d)",
+                    fn, kMaxTopK, kMaxExperts, T, k, E, Q);
+    if (!seq_offsets && Q != 1) return fail(MB_ERR_INVALID_ARG, "%s: no seq_offsets with Q = %d", fn, Q);
+    if (!aligned16(seq_offsets)) return fail(MB_ERR_INVALID_ARG, "%s: pointers must be 16-byte aligned", fn);
+    return MB_OK;
+}
+
+size_t moe_balance_workspace_size(int T, int E, int Q) {
+    if (!moe_boundary_supported(MB_STAGE_BALANCE, T, 0, E, 1, Q)) return 0;
+    return balance_workspace_bytes(T, E, Q);
+}
+
+int moe_balance_loss(const float* logits, const int32_t* topk_ids, const uint8_t* token_mask, int T, int E, int k,
+                     const int32_t* seq_offsets, int Q, float coeff, float* loss, int32_t* counts, float* prob_sums,
+                     int32_t* seq_tokens, void* workspace, size_t workspace_bytes, void* stream) {
+    const char* fn = "moe_balance_loss";
+    const int st = check_balance(fn, T, E, k, seq_offsets, Q);
+    if (st != MB_OK) return st;
+    if ((T > 0 && (!logits || !topk_ids || !token_mask)) || !loss || !counts || !prob_sums || !seq_tokens)
+        return fail(MB_ERR_INVALID_ARG, "%s: null pointer", fn);
+    if (!aligned16(logits) || !aligned16(topk_ids) || !aligned16(token_mask) || !aligned16(loss) ||
+        !aligned16(counts) || !aligned16(prob_sums) || !aligned16(seq_tokens))
+        return fail(MB_ERR_INVALID_ARG, "%s: pointers must be 16-byte aligned", fn);
+    const size_t need = balance_workspace_bytes(T, E, Q);
+    if (!workspace || workspace_bytes < need)
+        return fail(MB_ERR_INVALID_ARG, "%s: needs a workspace of %zu bytes (got %zu)", fn, need,
+                    workspace ? workspace_bytes : static_cast<size_t>(0));
+    if (!aligned16(workspace)) return fail(MB_ERR_INVALID_ARG, "%s: workspace must be 16-byte aligned", fn);
+    const BalanceLaunch b{logits, topk_ids, token_mask, seq_offsets, T, E, k, Q, coeff, loss, counts, prob_sums,
+                          seq_tokens, workspace};
+    return cuda_status(launch_balance_loss(b, static_cast<cudaStream_t>(stream)), fn);
+}
+
+int moe_route_backward(const float* logits, const int32_t* topk_ids, const uint8_t* token_mask, int T, int E, int k,
+                       const float* grad_weights, const float* grad_loss, float coeff, const int32_t* counts,
+                       const int32_t* seq_tokens, const int32_t* seq_offsets, int Q, float* grad_logits, void* stream) {
+    const char* fn = "moe_route_backward";
+    if (!grad_loss) Q = 1, seq_offsets = nullptr, counts = seq_tokens = nullptr;   // unused then
+    const int st = check_balance(fn, T, E, k, seq_offsets, Q);
+    if (st != MB_OK) return st;
+    if (T == 0) return MB_OK;
+    if (!grad_weights && !grad_loss)
+        return fail(MB_ERR_INVALID_ARG, "%s: neither grad_weights nor grad_loss is given", fn);
+    if (!logits || !topk_ids || !token_mask || !grad_logits || (grad_loss && (!counts || !seq_tokens)))
+        return fail(MB_ERR_INVALID_ARG, "%s: null pointer", fn);
+    if (!aligned16(logits) || !aligned16(topk_ids) || !aligned16(token_mask) || !aligned16(grad_weights) ||
+        !aligned16(counts) || !aligned16(seq_tokens) || !aligned16(grad_logits) ||
+        (reinterpret_cast<uintptr_t>(grad_loss) & 3u))
+        return fail(MB_ERR_INVALID_ARG, "%s: pointers must be 16-byte aligned", fn);
+    if (grad_logits == logits) return fail(MB_ERR_INVALID_ARG, "%s: grad_logits must not be logits", fn);
+    const GateGradLaunch b{logits, topk_ids, token_mask, T, E, k, grad_weights, grad_loss, coeff, counts, seq_tokens,
+                           seq_offsets, Q, grad_logits};
+    return cuda_status(launch_route_backward(b, static_cast<cudaStream_t>(stream)), fn);
 }
 
 // ------------------------------------------------------------------ finalize + all-reduce

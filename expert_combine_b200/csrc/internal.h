@@ -77,6 +77,39 @@ size_t dispatch_workspace_bytes(int64_t n, int E);
 cudaError_t launch_dispatch(const int32_t* ids, int T, int k, int e0, int E, int32_t* offsets, int32_t* row_idx,
                             int32_t* row_token, void* workspace, cudaStream_t s);
 
+// Balance loss of the router and the gradient of its logits (balance.cu).
+struct BalanceLaunch {
+    const float* logits;
+    const int32_t* ids;
+    const uint8_t* mask;
+    const int32_t* offsets;     // [Q + 1] or NULL: one sequence
+    int T, E, k, Q;
+    float coeff;
+    float* loss;
+    int32_t* counts;
+    float* prob_sums;
+    int32_t* seq_tokens;
+    void* workspace;
+};
+size_t balance_workspace_bytes(int T, int E, int Q);
+cudaError_t launch_balance_loss(const BalanceLaunch& b, cudaStream_t s);
+
+struct GateGradLaunch {
+    const float* logits;
+    const int32_t* ids;
+    const uint8_t* mask;
+    int T, E, k;
+    const float* grad_w;        // NULL: no gradient from the gate's weights
+    const float* grad_loss;     // NULL: none from the balance loss (the rest is then unused)
+    float coeff;
+    const int32_t* counts;
+    const int32_t* seq_tokens;
+    const int32_t* offsets;
+    int Q;
+    float* grad;
+};
+cudaError_t launch_route_backward(const GateGradLaunch& b, cudaStream_t s);
+
 // Largest H the row kernels take (16-element blocks, at most 1024 per row).
 constexpr int kMaxHidden = 16384;
 constexpr int kMaxTopK = 32;

@@ -11,3 +11,4 @@
 #include "dispatch.cu"
 #include "dispatch_noalloc.cu"
 #include "finalize_ar.cu"
+#include "balance.cu"

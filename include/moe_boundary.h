@@ -5,7 +5,8 @@
  *
  * Entry points: moe_route, norm_quant_nvfp4, moe_route_norm_quant (both
  * pre-expert stages in one call), expert_combine, residual_join,
- * expert_combine_join (the combine with the join fused), moe_dispatch and
+ * expert_combine_join (the combine with the join fused), moe_balance_loss and
+ * moe_route_backward (training the router gate), moe_dispatch and
  * moe_dispatch_noalloc (expert-grouped rows of the routing entries),
  * router_weight_prepare and router_logits (the router projection),
  * expert_finalize_allreduce and expert_finalize_allreduce_local (the combine
@@ -225,6 +226,76 @@ int expert_combine_join(const uint16_t* expert_out, int64_t num_rows, int H, con
                         uint16_t* next_prenorm, void* stream);
 
 /*
+ * moe_balance_loss -- per-expert counts and the sequence-wise balance loss of
+ * the router gate.
+ *
+ * No counterpart on the reference pages, which serve the router: what its
+ * training adds to the logits and picks that moe_route reads and writes.
+ *
+ * The batch is Q sequences: sequence q is the tokens seq_offsets[q] <= t <
+ * seq_offsets[q + 1] with token_mask[t] != 0 (seq_offsets NULL: Q = 1, all T
+ * tokens).  Tokens of no sequence and invalid tokens take no part and their
+ * logits are not used (they may hold NaN).  With s = sigmoid(logits):
+ *   counts[q, e]    = picks of expert e by q's tokens (ids outside [0, E) are
+ *                     skipped, a repeated id counts each time)
+ *   prob_sums[q, e] = sum over q's tokens of s_e / (s_0 + ... + s_{E-1})
+ *   seq_tokens[q]   = n_q, the valid tokens of q
+ *   loss            = coeff / Q' * sum_q E / (k n_q^2)
+ *                     * sum_e counts[q, e] * prob_sums[q, e]
+ * over the Q' sequences that have a valid token (0 when none has).  A token
+ * whose logits are all -inf adds nothing to prob_sums.  The probabilities are
+ * formed relative to the token's largest sigmoid, so logits far below zero
+ * keep theirs.
+ *
+ *   logits      [T, E] FP32         topk_ids    [T, k] int32 (moe_route's)
+ *   token_mask  [T] uint8           seq_offsets [Q + 1] int32 on the device,
+ *                                   ascending in [0, T], or NULL with Q = 1
+ *   loss        [1] FP32 (out)      counts      [Q, E] int32 (out)
+ *   prob_sums   [Q, E] FP32 (out)   seq_tokens  [Q] int32 (out)
+ *   workspace   device scratch of moe_balance_workspace_size(T, E, Q) bytes,
+ *               16-byte aligned; needs no initialisation; two calls that
+ *               overlap on the GPU need two
+ * Sums are FP32 in an order fixed by the sizes (no floating-point atomics).
+ * Offsets that are not ascending give undefined outputs, never an access out
+ * of bounds.  T == 0 writes zeros (topk_ids, logits and token_mask may then be
+ * NULL).
+ * Supported: 1 <= k <= 32, k <= E <= 4096, T * k < 2^31, T <= 2^30,
+ * 1 <= Q <= 2^20, Q * E < 2^31.
+ */
+size_t moe_balance_workspace_size(int T, int E, int Q);
+int moe_balance_loss(const float* logits, const int32_t* topk_ids, const uint8_t* token_mask, int T, int E, int k,
+                     const int32_t* seq_offsets, int Q, float coeff, float* loss, int32_t* counts, float* prob_sums,
+                     int32_t* seq_tokens, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * moe_route_backward -- the gradient of the router's logits, from the
+ * gradients of the gate's weights and of the balance loss.
+ *
+ * No counterpart on the reference pages (see moe_balance_loss).
+ *
+ * For a valid token t, S = s_0 + ... + s_{E-1}:
+ *   gate (grad_weights != NULL), over the token's picks inside [0, E), whose
+ *   weights are w_j = s_j / (sum of their s; formed again from the logits):
+ *     grad[t, ids_j] += w_j (1 - s_j) (grad_weights[t, j] - sum_i grad_weights[t, i] w_i)
+ *     (an expert picked twice gets the sum of both)
+ *   balance (grad_loss != NULL), t in sequence q:
+ *     g_e = grad_loss * coeff / Q' * E / (k n_q^2) * counts[q, e]
+ *     grad[t, e] += (g_e - sum_i g_i s_i / S) * s_e (1 - s_e) / S
+ *     (the counts are constants)
+ * The selection bias gets no gradient: it only selects.  Rows of invalid
+ * tokens are zero.  counts, seq_tokens, seq_offsets, Q and coeff are those of
+ * the moe_balance_loss call, and unused when grad_loss is NULL.
+ *
+ *   grad_weights [T, k] FP32 or NULL     grad_loss [1] FP32 on the device or NULL
+ *   grad_logits  [T, E] FP32 (out; every element is written; not logits)
+ * At least one of the two incoming gradients is given.  Supported: as
+ * moe_balance_loss.
+ */
+int moe_route_backward(const float* logits, const int32_t* topk_ids, const uint8_t* token_mask, int T, int E, int k,
+                       const float* grad_weights, const float* grad_loss, float coeff, const int32_t* counts,
+                       const int32_t* seq_tokens, const int32_t* seq_offsets, int Q, float* grad_logits, void* stream);
+
+/*
  * router_weight_prepare -- the FP32 router weight in the form router_logits
  * reads: three BF16 parts of each weight (done once, when the weight loads).
  *
@@ -420,6 +491,7 @@ enum {
     MB_STAGE_DISPATCH = 6,
     MB_STAGE_ROUTER_LOGITS = 7,
     MB_STAGE_FINALIZE_AR = 8,   /* tp = world */
+    MB_STAGE_BALANCE = 9,       /* moe_balance_loss and moe_route_backward; tp = Q */
 };
 
 /*
