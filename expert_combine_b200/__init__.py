@@ -21,6 +21,7 @@ from ._lib import (  # noqa: F401
     STAGE_DISPATCH,
     STAGE_FINALIZE_AR,
     STAGE_JOIN,
+    STAGE_LORA,
     STAGE_NORM_QUANT,
     STAGE_ROUTE,
     STAGE_ROUTE_NORM_QUANT,
@@ -42,6 +43,8 @@ from ._lib import (  # noqa: F401
     last_error,
     lib_path,
     load,
+    lora_add,
+    lora_workspace_size,
     moe_balance_loss,
     moe_dispatch,
     moe_dispatch_noalloc,

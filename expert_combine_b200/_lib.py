@@ -64,6 +64,7 @@ STAGE_DISPATCH = 6
 STAGE_ROUTER_LOGITS = 7
 STAGE_FINALIZE_AR = 8
 STAGE_BALANCE = 9
+STAGE_LORA = 10
 FAR_MAX_WORLD = 8
 IPC_HANDLE_BYTES = 64
 
@@ -115,6 +116,7 @@ def load() -> ctypes.CDLL:
                 "moe_dispatch_noalloc": [P, i32, i32, i32, i32, P, P, P, P],
                 "moe_balance_loss": [P, P, P, i32, i32, i32, P, i32, f32, P, P, P, P, P, ctypes.c_size_t, P],
                 "moe_route_backward": [P, P, P, i32, i32, i32, P, P, f32, P, P, P, i32, P, P],
+                "lora_add": [P, i32, P, i32, i32, P, P, i32, i32, i32, P, P, P, P, ctypes.c_size_t, P],
                 "router_logits": [P, i32, i32, P, i32, f32, P, P],
                 "router_weight_prepare": [P, i32, i32, P, P],
                 "moe_boundary_supported": [i32, i32, i32, i32, i32, i32],
@@ -136,6 +138,8 @@ def load() -> ctypes.CDLL:
                 fn.restype = ctypes.c_char_p if name == "mb_last_error" else ctypes.c_int
             lib.moe_dispatch_workspace_size.argtypes = [i32, i32, i32]
             lib.moe_dispatch_workspace_size.restype = ctypes.c_size_t
+            lib.lora_workspace_size.argtypes = [i32, i32, i32, i32, i32]
+            lib.lora_workspace_size.restype = ctypes.c_size_t
             lib.moe_balance_workspace_size.argtypes = [i32, i32, i32]
             lib.moe_balance_workspace_size.restype = ctypes.c_size_t
             lib.finalize_ar_workspace_size.argtypes = [i32, i32, i32]
@@ -610,6 +614,51 @@ def router_logits(x: torch.Tensor, w3: torch.Tensor, scale: float = 1.0,
     _check("router_logits", load().router_logits(_ptr(x), T, H, _ptr(w3), E, float(scale), _ptr(logits),
                                                  _stream(stream)))
     return logits
+
+
+def lora_workspace_size(T: int, H: int, N: int, R: int, L: int) -> int:
+    """Bytes of device workspace lora_add needs (0 when the sizes are not supported)."""
+    return int(load().lora_workspace_size(T, H, N, R, L))
+
+
+@_traced
+def lora_add(base: torch.Tensor, x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, adapter_ids: torch.Tensor,
+             scales: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+             workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Low-rank adapters of many requests beside a projection: out [T, N] =
+    base + scales[i] * (x A_i^T) B_i^T with i = adapter_ids[t] (int32; outside
+    [0, L): the row of base).
+
+    base and out are float32 or bfloat16, x [T, H], a [L, R, H] and b [L, N, R]
+    bfloat16.  ``out=base`` works in place; without ``out`` a tensor is
+    allocated, and so is ``workspace`` (uint8, ``lora_workspace_size`` bytes)."""
+    fn = "lora_add"
+    bf16 = base.dtype == torch.bfloat16
+    _want(base, torch.bfloat16 if bf16 else torch.float32, "base")
+    _want(x, torch.bfloat16, "x")
+    _want(a, torch.bfloat16, "a")
+    _want(b, torch.bfloat16, "b")
+    _want(adapter_ids, torch.int32, "adapter_ids")
+    if scales is not None:
+        _want(scales, torch.float32, "scales")
+    T, H = x.shape
+    L, R = a.shape[:2]
+    N = base.shape[1]
+    if a.shape != (L, R, H) or b.shape != (L, N, R) or base.shape != (T, N) or adapter_ids.numel() != T or (
+            scales is not None and scales.numel() != L):
+        raise ValueError(f"{fn}: shape mismatch")
+    if out is None:
+        out = torch.empty_like(base)
+    _want(out, base.dtype, "out")
+    if out.shape != base.shape:
+        raise ValueError(f"{fn}: shape mismatch")
+    if workspace is None:
+        workspace = torch.empty(lora_workspace_size(T, H, N, R, L), dtype=torch.uint8, device=base.device)
+    _want(workspace, torch.uint8, "workspace")
+    with _on(fn, base, x, a, b, adapter_ids, scales, out, workspace):
+        _check(fn, load().lora_add(_ptr(base), int(bf16), _ptr(x), T, H, _ptr(a), _ptr(b), N, R, L, _ptr(adapter_ids),
+                                   _ptr(scales), _ptr(out), _ptr(workspace), workspace.numel(), _stream(stream)))
+    return out
 
 
 # ---------------------------------------------------------------------------- finalize + all-reduce

@@ -84,6 +84,12 @@ int moe_boundary_supported(int stage, int T, int H, int E, int k, int tp) {
                     static_cast<int64_t>(T) * k <= INT32_MAX)
                        ? 1
                        : 0;
+        case MB_STAGE_LORA:
+            return (H >= 8 && H % 8 == 0 && H <= 65536 && E >= 8 && E % 8 == 0 && E <= 262144 && k >= 8 && k % 8 == 0 &&
+                    k <= kMaxLoraRank && tp >= 1 && tp <= kMaxExperts && static_cast<int64_t>(tp) * E <= INT32_MAX &&
+                    T <= (1 << 24))
+                       ? 1
+                       : 0;
         case MB_STAGE_BALANCE:
             return (k >= 1 && k <= kMaxTopK && E >= k && E <= kMaxExperts && T <= (1 << 30) &&
                     static_cast<int64_t>(T) * k <= INT32_MAX && tp >= 1 && tp <= (1 << 20) &&
@@ -331,6 +337,46 @@ int moe_dispatch(const int32_t* topk_ids, int T, int k, int expert_begin, int E,
     return cuda_status(launch_dispatch(topk_ids, T, k, expert_begin, E, expert_offsets, row_idx, row_token,
                                        workspace, static_cast<cudaStream_t>(stream)),
                        fn);
+}
+
+// ------------------------------------------------------------------ low-rank adapters
+size_t lora_workspace_size(int T, int H, int N, int R, int L) {
+    if (!moe_boundary_supported(MB_STAGE_LORA, T, H, N, R, L)) return 0;
+    return lora_workspace_bytes(T, H, N, R, L);
+}
+
+static bool overlap(const void* p, size_t n, const void* q, size_t m) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+    return a < b + m && b < a + n;
+}
+
+int lora_add(const void* base, int base_bf16, const uint16_t* x, int T, int H, const uint16_t* a, const uint16_t* b,
+             int N, int R, int L, const int32_t* adapter_ids, const float* scales, void* out, void* workspace,
+             size_t workspace_bytes, void* stream) {
+    const char* fn = "lora_add";
+    if (T < 0 || H < 0 || N < 0 || R < 0 || L < 0) return fail(MB_ERR_INVALID_ARG, "%s: negative size", fn);
+    if (base_bf16 != 0 && base_bf16 != 1) return fail(MB_ERR_INVALID_ARG, "%s: base_bf16 must be 0 or 1", fn);
+    if (!moe_boundary_supported(MB_STAGE_LORA, T, H, N, R, L))
+        return fail(MB_ERR_UNSUPPORTED,
+                    "%s: needs H, N and R in steps of 8, H <= 65536, N <= 262144, R <= %d, 1 <= L <= %d, L * N < 2^31 "
+                    "and T <= 2^24 (T=%d, H=%d, N=%d, R=%d, L=%d)",
+                    fn, kMaxLoraRank, kMaxExperts, T, H, N, R, L);
+    if (T == 0) return MB_OK;
+    if (!base || !x || !a || !b || !adapter_ids || !out) return fail(MB_ERR_INVALID_ARG, "%s: null pointer", fn);
+    if (!aligned16(base) || !aligned16(x) || !aligned16(a) || !aligned16(b) || !aligned16(adapter_ids) ||
+        !aligned16(scales) || !aligned16(out))
+        return fail(MB_ERR_INVALID_ARG, "%s: pointers must be 16-byte aligned", fn);
+    const size_t nout = static_cast<size_t>(T) * N * (base_bf16 ? 2 : 4), l = static_cast<size_t>(L) * R * 2;
+    if ((out != base && overlap(out, nout, base, nout)) || overlap(out, nout, x, static_cast<size_t>(T) * H * 2) ||
+        overlap(out, nout, a, l * H) || overlap(out, nout, b, l * N))
+        return fail(MB_ERR_INVALID_ARG, "%s: out overlaps an input (only out == base is allowed)", fn);
+    const size_t need = lora_workspace_bytes(T, H, N, R, L);
+    if (!workspace || workspace_bytes < need)
+        return fail(MB_ERR_INVALID_ARG, "%s: needs a workspace of %zu bytes (got %zu)", fn, need,
+                    workspace ? workspace_bytes : static_cast<size_t>(0));
+    if (!aligned256(workspace)) return fail(MB_ERR_INVALID_ARG, "%s: workspace must be 256-byte aligned", fn);
+    const LoraLaunch ll{base, out, base_bf16 != 0, x, a, b, adapter_ids, scales, T, H, N, R, L, workspace};
+    return cuda_status(launch_lora_add(ll, static_cast<cudaStream_t>(stream)), fn);
 }
 
 // ------------------------------------------------------------------ training the router

@@ -110,6 +110,23 @@ struct GateGradLaunch {
 };
 cudaError_t launch_route_backward(const GateGradLaunch& b, cudaStream_t s);
 
+// Low-rank adapters beside a projection (lora.cu).
+constexpr int kMaxLoraRank = 128;
+struct LoraLaunch {
+    const void* base;           // [T, N] FP32 or BF16
+    void* out;                  // as base; may be base
+    bool bf16;
+    const uint16_t* x;          // [T, H]
+    const uint16_t* a;          // [L, R, H]
+    const uint16_t* b;          // [L, N, R]
+    const int32_t* ids;         // [T]
+    const float* scales;        // [L] or NULL
+    int T, H, N, R, L;
+    void* workspace;
+};
+size_t lora_workspace_bytes(int T, int H, int N, int R, int L);
+cudaError_t launch_lora_add(const LoraLaunch& l, cudaStream_t s);
+
 // Largest H the row kernels take (16-element blocks, at most 1024 per row).
 constexpr int kMaxHidden = 16384;
 constexpr int kMaxTopK = 32;

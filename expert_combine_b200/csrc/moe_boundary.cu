@@ -12,3 +12,4 @@
 #include "dispatch_noalloc.cu"
 #include "finalize_ar.cu"
 #include "balance.cu"
+#include "lora.cu"

@@ -8,7 +8,8 @@
  * expert_combine_join (the combine with the join fused), moe_balance_loss and
  * moe_route_backward (training the router gate), moe_dispatch and
  * moe_dispatch_noalloc (expert-grouped rows of the routing entries),
- * router_weight_prepare and router_logits (the router projection),
+ * router_weight_prepare and router_logits (the router projection), lora_add
+ * (low-rank adapters beside a projection),
  * expert_finalize_allreduce and expert_finalize_allreduce_local (the combine
  * of an expert-parallel layer fused with its tensor-parallel all-reduce) with
  * their workspace calls and the mb_ipc_* peer-memory helpers; queries
@@ -337,6 +338,36 @@ int router_logits(const uint16_t* x, int T, int H, const uint16_t* w3, int E, fl
                   void* stream);
 
 /*
+ * lora_add -- low-rank adapters of many requests beside a shared projection
+ * (router_logits, or any projection of the caller's).
+ *
+ * No counterpart on the reference pages.
+ *
+ *   out[t, n] = base[t, n] + scales[a] * sum_r v[t, r] * B[a, n, r],
+ *   v[t, r]   = sum_h x[t, h] * A[a, r, h],   a = adapter_ids[t]
+ * A token whose id lies outside [0, L) (-1: a request without an adapter)
+ * gets out[t, :] = base[t, :], and its x is not read.  Adapters of fewer than
+ * R ranks are padded with zero rows of A or zero columns of B.
+ *
+ *   base  [T, N] FP32 or BF16 (base_bf16 = 0 or 1)    x  [T, H] BF16
+ *   out   [T, N] of base's type (out): base itself (in place) or memory apart
+ *         from base, x, a and b
+ *   a  [L, R, H] BF16       b  [L, N, R] BF16
+ *   adapter_ids  [T] int32  scales  [L] FP32, or NULL for 1
+ *   workspace  device scratch of lora_workspace_size(T, H, N, R, L) bytes,
+ *              256-byte aligned; needs no initialisation; two calls that
+ *              overlap on the GPU need two
+ * v and the sums over r are FP32 (products of BF16 values are exact in FP32),
+ * out is rounded once.  No atomics: results are the same run to run.
+ * Supported: H % 8 == 0, 8 <= H <= 65536, N % 8 == 0, 8 <= N <= 262144,
+ * R % 8 == 0, 8 <= R <= 128, 1 <= L <= 4096, L * N < 2^31, T <= 2^24.
+ */
+size_t lora_workspace_size(int T, int H, int N, int R, int L);
+int lora_add(const void* base, int base_bf16, const uint16_t* x, int T, int H, const uint16_t* a, const uint16_t* b,
+             int N, int R, int L, const int32_t* adapter_ids, const float* scales, void* out, void* workspace,
+             size_t workspace_bytes, void* stream);
+
+/*
  * moe_dispatch -- expert-grouped rows of the routing entries: the dispatch
  * step between the router (moe_route) and the experts, producing the
  * row_idx that expert_combine reads.
@@ -491,6 +522,7 @@ enum {
     MB_STAGE_DISPATCH = 6,
     MB_STAGE_ROUTER_LOGITS = 7,
     MB_STAGE_FINALIZE_AR = 8,   /* tp = world */
+    MB_STAGE_LORA = 10,         /* lora_add; E = N, k = R, tp = L */
     MB_STAGE_BALANCE = 9,       /* moe_balance_loss and moe_route_backward; tp = Q */
 };
 
