@@ -161,9 +161,15 @@ def _ptr(t: Optional[torch.Tensor]):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
+def _raw_stream(dev: int) -> int:
+    """Address of the device's current stream (torch.cuda.current_stream builds a
+    Stream object on the way, several microseconds of a small call)."""
+    return torch._C._cuda_getCurrentRawStream(dev)
+
+
 def _stream(stream) -> ctypes.c_void_p:
     if stream is None:
-        stream = torch.cuda.current_stream()
+        return ctypes.c_void_p(_raw_stream(torch.cuda.current_device()))
     return ctypes.c_void_p(stream.cuda_stream)
 
 
@@ -176,27 +182,25 @@ def _want(t: torch.Tensor, dtype: torch.dtype, name: str) -> None:
         raise ValueError(f"{name}: expected a contiguous tensor")
 
 
-class _on:
-    """The tensors' device as the current one, for calls whose tensors may live on another."""
+def _at(t: Optional[torch.Tensor]) -> Optional[int]:
+    return None if t is None else t.data_ptr()
 
-    __slots__ = ("dev", "guard")
 
-    def __init__(self, fn: str, first: torch.Tensor, *rest: Optional[torch.Tensor]):
-        self.dev = first.device
-        for t in rest:
-            if t is not None and t.device != self.dev:
-                raise ValueError(f"{fn}: tensors on {self.dev} and {t.device}")
-
-    def __enter__(self):
-        self.guard = None
-        if self.dev.index != torch.cuda.current_device():
-            self.guard = torch.cuda.device(self.dev)
-            self.guard.__enter__()
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
-        return False
+def _enqueue(name: str, tensors, stream, *args) -> None:
+    """The call ``name(*args, stream)`` with the tensors' device as the current
+    one (they must share it); ``stream`` None is that device's current stream."""
+    dev = tensors[0].get_device()
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"{name}: tensors on devices {dev} and {t.get_device()}")
+    fn = getattr(_lib or load(), name)
+    if dev == torch._C._cuda_getDevice():
+        status = fn(*args, _raw_stream(dev) if stream is None else stream.cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, _raw_stream(dev) if stream is None else stream.cuda_stream)
+    if status != 0:
+        raise MoEBoundaryError(name, status, last_error())
 
 
 def supported(stage: int, T: int = 1, H: int = 16, E: int = 1, k: int = 1, tp: int = 1) -> bool:
@@ -537,10 +541,9 @@ def moe_balance_loss(logits: torch.Tensor, topk_ids: torch.Tensor, token_mask: t
         _want(t, dt, name)
     if loss.numel() != 1 or counts.shape != (Q, E) or prob_sums.shape != (Q, E) or seq_tokens.numel() != Q:
         raise ValueError(f"{fn}: shape mismatch")
-    with _on(fn, logits, topk_ids, token_mask, seq_offsets, loss, counts, prob_sums, seq_tokens, workspace):
-        _check(fn, load().moe_balance_loss(_ptr(logits), _ptr(topk_ids), _ptr(token_mask), T, E, k, _ptr(seq_offsets),
-                                           Q, float(coeff), _ptr(loss), _ptr(counts), _ptr(prob_sums),
-                                           _ptr(seq_tokens), _ptr(workspace), workspace.numel(), _stream(stream)))
+    _enqueue(fn, (logits, topk_ids, token_mask, loss, counts, prob_sums, seq_tokens, workspace, seq_offsets), stream,
+             _at(logits), _at(topk_ids), _at(token_mask), T, E, k, _at(seq_offsets), Q, coeff, _at(loss), _at(counts),
+             _at(prob_sums), _at(seq_tokens), _at(workspace), workspace.numel())
     return loss, counts, prob_sums, seq_tokens
 
 
@@ -573,11 +576,9 @@ def moe_route_backward(logits: torch.Tensor, topk_ids: torch.Tensor, token_mask:
     _want(grad_logits, torch.float32, "grad_logits")
     if grad_logits.shape != (T, E):
         raise ValueError(f"{fn}: shape mismatch")
-    with _on(fn, logits, topk_ids, token_mask, grad_weights, grad_loss, counts, seq_tokens, seq_offsets, grad_logits):
-        _check(fn, load().moe_route_backward(_ptr(logits), _ptr(topk_ids), _ptr(token_mask), T, E, k,
-                                             _ptr(grad_weights), _ptr(grad_loss), float(coeff), _ptr(counts),
-                                             _ptr(seq_tokens), _ptr(seq_offsets), Q, _ptr(grad_logits),
-                                             _stream(stream)))
+    _enqueue(fn, (logits, topk_ids, token_mask, grad_logits, grad_weights, grad_loss, counts, seq_tokens, seq_offsets),
+             stream, _at(logits), _at(topk_ids), _at(token_mask), T, E, k, _at(grad_weights), _at(grad_loss), coeff,
+             _at(counts), _at(seq_tokens), _at(seq_offsets), Q, _at(grad_logits))
     return grad_logits
 
 
@@ -655,9 +656,8 @@ def lora_add(base: torch.Tensor, x: torch.Tensor, a: torch.Tensor, b: torch.Tens
     if workspace is None:
         workspace = torch.empty(lora_workspace_size(T, H, N, R, L), dtype=torch.uint8, device=base.device)
     _want(workspace, torch.uint8, "workspace")
-    with _on(fn, base, x, a, b, adapter_ids, scales, out, workspace):
-        _check(fn, load().lora_add(_ptr(base), int(bf16), _ptr(x), T, H, _ptr(a), _ptr(b), N, R, L, _ptr(adapter_ids),
-                                   _ptr(scales), _ptr(out), _ptr(workspace), workspace.numel(), _stream(stream)))
+    _enqueue(fn, (base, x, a, b, adapter_ids, scales, out, workspace), stream, _at(base), int(bf16), _at(x), T, H,
+             _at(a), _at(b), N, R, L, _at(adapter_ids), _at(scales), _at(out), _at(workspace), workspace.numel())
     return out
 
 
