@@ -20,8 +20,28 @@
 // group split H; each CTA writes its partial v, and the expand kernel adds the
 // partials in order (no atomics), scales them once, and holds one group's v in
 // shared memory while each thread forms two columns with FP32 multiply-adds.
+//
+// Many tokens (prefill).  The tokens are grouped by adapter with the dispatch
+// of the routing entries (one "pick" a token, L "experts"), each adapter's run
+// is cut into tiles of 128 tokens, and both products run on the tensor cores
+// (tcgen05, accumulators in tensor memory), one persistent CTA per SM: a TMA
+// warp, an MMA thread and eight epilogue warps.
+//   shrink  All tiles' slabs of 64 k form one line that is cut into equal
+//     pieces, one per CTA, so the SMs finish together whatever the sizes of
+//     the groups.  The rows of a tile lie anywhere in x: 32 lanes fetch four
+//     each (gather4).  A tile that several CTAs share is summed by the one that
+//     arrives last, from the partials, in the CTAs' order (an integer counter
+//     per tile; the sum's order does not depend on the arrival).  It writes v
+//     scaled and split into BF16 parts (3 for FP32 outputs: 2^-24 of v is left;
+//     2 for BF16 outputs: 2^-16), in the layout of the next MMA's operand.
+//   expand  Work items are a tile x 128 columns, cut the same way.  D = sum
+//     over the parts v_p B^T; base arrives by gather4 in the swizzled layout in
+//     which an epilogue thread reads its row without bank conflicts, the sum
+//     replaces it there, and the warp writes whole 128-byte rows of out.
 #include "internal.h"
 #include "common.cuh"
+#include "tmap.h"
+#include "tmem.cuh"
 
 namespace mb {
 
@@ -256,45 +276,712 @@ cudaError_t lora_launch(F* kernel, dim3 grid, int threads, const LoraArgs& a, cu
     return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
+// ------------------------------------------------------------------ many tokens
+constexpr int kLmTile = 128;                 // tokens per tile (M of the MMAs)
+constexpr int kLmSlab = 64;                  // k per slab: 128 bytes of BF16
+constexpr int kLmSlabBytes = kLmTile * 128;  // 16 KB
+constexpr int kLmCols = 128;                 // columns of out per work item
+constexpr int kLmThreads = 12 * 32;          // TMA, MMA, two that copy rows without an adapter, 8 epilogue warps
+constexpr int kLmEpiWarps = 8;
+constexpr int kLmBytes = 208 * 1024;         // ring buffers of a CTA
+constexpr int kLmMaxStages = 12;
+constexpr unsigned int kLmTimeout = 32u;     // bit 5 of the device status word
+
+struct LmTile {
+    int adapter, row0, count, pad;           // rows row0 .. row0 + count - 1 of the grouped order
+};
+
+struct LmArgs {
+    const int32_t* offsets;      // [L + 1] first row of each adapter's group
+    const int32_t* row_idx;      // [T] row of a token, -1: no adapter
+    const int32_t* row_token;    // [T] token of a row
+    LmTile* tiles;
+    int32_t* ntiles;             // [1]
+    int32_t* arrived;            // [tiles] CTAs that have left their partial
+    float* part;                 // [SMs + tiles][R][128]
+    uint16_t* v;                 // [tiles][parts][ks][128][64]
+    const float* scales;
+    const void* base;
+    void* out;
+    int T, H, N, R, L;
+    int rn;                      // R in steps of 16: columns of the shrink's accumulator
+    int ks;                      // 64-wide slabs of R
+    int parts;                   // BF16 parts of v
+    int stages, b_stages, base_stages, v_bufs;
+};
+
+// Tiles of 128 rows of every adapter's group.
+__global__ void __launch_bounds__(1024) lora_tiles_kernel(const LmArgs a) {
+    __shared__ int s_first[kMaxExperts];     // first tile of each adapter
+    __shared__ int s_warp[32];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    constexpr int kPer = kMaxExperts / 1024;
+    griddep_wait();
+    griddep_launch();
+    int n[kPer], sum = 0;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+        const int e = tid * kPer + j;
+        n[j] = e < a.L ? (a.offsets[e + 1] - a.offsets[e] + kLmTile - 1) / kLmTile : 0;
+        sum += n[j];
+    }
+    int scan = sum;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const int o = __shfl_up_sync(0xffffffffu, scan, off);
+        if (lane >= off) scan += o;
+    }
+    if (lane == 31) s_warp[warp] = scan;
+    __syncthreads();
+    int before = 0, total = 0;
+    for (int w = 0; w < 32; ++w) {
+        if (w < warp) before += s_warp[w];
+        total += s_warp[w];
+    }
+    int first = before + scan - sum;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+        s_first[tid * kPer + j] = first;
+        first += n[j];
+    }
+    __syncthreads();
+    if (tid == 0) *a.ntiles = total;
+    for (int i = tid; i < total; i += 1024) a.arrived[i] = 0;
+    for (int e = warp; e < a.L; e += 32) {
+        const int lo = a.offsets[e], hi = a.offsets[e + 1];
+        for (int i = lane; lo + i * kLmTile < hi; i += 32) {
+            const int row0 = lo + i * kLmTile;
+            a.tiles[s_first[e] + i] = LmTile{e, row0, min(kLmTile, hi - row0), 0};
+        }
+    }
+}
+
+// Four rows of a 2-D tensor, 128 bytes of each, to shared memory.
+__device__ __forceinline__ void tma_gather4(uint32_t dst, const void* tmap, int x, int4 r, uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
+        "l"(tmap), "r"(x), "r"(r.x), "r"(r.y), "r"(r.z), "r"(r.w), "r"(smem_addr(bar))
+        : "memory");
+}
+
+// The tokens of rows 4 lane .. 4 lane + 3 of a tile; rows behind its end
+// repeat the first (fetched, never used).
+__device__ __forceinline__ int4 lm_rows(const LmArgs& a, const LmTile& t, int lane) {
+    const int32_t* p = a.row_token + t.row0;
+    const int i = 4 * lane;
+    int4 r;
+    r.x = p[i < t.count ? i : 0];
+    r.y = p[i + 1 < t.count ? i + 1 : 0];
+    r.z = p[i + 2 < t.count ? i + 2 : 0];
+    r.w = p[i + 3 < t.count ? i + 3 : 0];
+    return r;
+}
+
+__device__ __forceinline__ uint32_t lm_idesc(int n) {   // FP32 += BF16 x BF16, both K-major, M = 128
+    return (1u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(n >> 3) << 17) |
+           (static_cast<uint32_t>(kLmTile >> 4) << 24);
+}
+
+// A ring position: slot and phase parity.
+struct Ring {
+    int slot = 0, phase = 0;
+    __device__ __forceinline__ void next(int n) {
+        if (++slot == n) slot = 0, phase ^= 1;
+    }
+};
+
+// Waits (bounded) until the last copy issued into each slot of a ring has landed.
+__device__ __forceinline__ void lm_drain(uint64_t* full, int n, int issued) {
+    for (int j = issued > n ? issued - n : 0; j < issued; ++j)
+        mbar_wait_bounded(&full[j % n], static_cast<uint32_t>((j / n) & 1), kLmTimeout);
+}
+
+// v of 16 ranks from group gi of one row: scaled, split, written as operand rows.
+__device__ __forceinline__ void lm_write_v(const LmArgs& a, int tile, int gi, int row, float scale, float (&v)[16]) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = 16 * gi + i < a.R ? v[i] * scale : 0.0f;
+    for (int p = 0; p < a.parts; ++p) {
+        uint32_t w[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            w[i] = pack_bf16x2_rn(make_float2(v[2 * i], v[2 * i + 1]));
+            const float2 b = unpack_bf16x2(w[i]);
+            // the rest is exact; behind an infinity or NaN nothing is left
+            v[2 * i] = fabsf(b.x) < INFINITY ? v[2 * i] - b.x : 0.0f;
+            v[2 * i + 1] = fabsf(b.y) < INFINITY ? v[2 * i + 1] - b.y : 0.0f;
+        }
+        uint16_t* dst = a.v + (((static_cast<size_t>(tile) * a.parts + p) * a.ks + gi / 4) * kLmTile + row) * kLmSlab +
+                        gi % 4 * 16;
+        st_v4(dst, make_uint4(w[0], w[1], w[2], w[3]));
+        st_v4(dst + 8, make_uint4(w[4], w[5], w[6], w[7]));
+    }
+}
+
+__global__ void __launch_bounds__(kLmThreads) lora_shrink_kernel(const __grid_constant__ CUtensorMap xmap,
+                                                                 const __grid_constant__ CUtensorMap amap,
+                                                                 const LmArgs a) {
+    extern __shared__ uint8_t lm_raw[];
+    const uint32_t raw = smem_addr(lm_raw);
+    uint8_t* ring = lm_raw + (((raw + 1023u) & ~1023u) - raw);
+    __shared__ __align__(8) uint64_t full[kLmMaxStages], empty[kLmMaxStages], acc_full[2], acc_empty[2], done;
+    __shared__ uint32_t s_tmem;
+    __shared__ int s_issued, s_last;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int S = a.stages, stage_bytes = kLmSlabBytes + a.rn * 128;
+    const uint32_t cols = a.rn <= 16 ? 32u : a.rn <= 32 ? 64u : a.rn <= 64 ? 128u : 256u;   // two accumulators
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < S; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&acc_full[i], 1);
+            mbar_init(&acc_empty[i], kLmEpiWarps);
+        }
+        mbar_init(&done, 1);
+        s_issued = 0;
+        fence_mbar_init();
+    }
+    if (warp == 0) {
+        tmem_alloc(&s_tmem, cols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = s_tmem;
+    griddep_wait();
+    griddep_launch();
+
+    const int J = (a.H + kLmSlab - 1) / kLmSlab;
+    const int64_t U = static_cast<int64_t>(*a.ntiles) * J, G = min(static_cast<int64_t>(gridDim.x), U);
+    const bool works = blockIdx.x < G;       // every working CTA has at least one slab
+    const int64_t u0 = works ? U * blockIdx.x / G : 0, u1 = works ? U * (blockIdx.x + 1) / G : 0;
+
+    if (warp == 0) {
+        Ring r;
+        int issued = 0;
+        bool ok = true;
+        for (int64_t u = u0; ok && u < u1;) {
+            const int tile = static_cast<int>(u / J), j0 = static_cast<int>(u % J);
+            const int j1 = static_cast<int>(min(static_cast<int64_t>(J), j0 + (u1 - u)));
+            const LmTile t = a.tiles[tile];
+            const int4 rows = lm_rows(a, t, lane);
+            const int quads = (t.count + 3) / 4;
+            for (int j = j0; j < j1; ++j) {
+                ok = issued < S || mbar_wait_bounded(&empty[r.slot], static_cast<uint32_t>(r.phase ^ 1), kLmTimeout);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                uint8_t* st = ring + static_cast<size_t>(r.slot) * stage_bytes;
+                if (lane == 0)
+                    mbar_arrive_expect_tx(&full[r.slot], static_cast<uint32_t>(quads * 512 + a.rn * 128));
+                __syncwarp();
+                if (lane < quads) tma_gather4(smem_addr(st) + 512 * lane, &xmap, j * kLmSlab, rows, &full[r.slot]);
+                if (lane == 0)
+                    tma_load_2d(smem_addr(st + kLmSlabBytes), &amap, j * kLmSlab, t.adapter * a.R, &full[r.slot]);
+                ++issued;
+                r.next(S);
+            }
+            u += j1 - j0;
+        }
+        if (lane == 0) s_issued = issued;
+        __syncwarp();
+    } else if (warp == 1) {
+        if (lane == 0) {
+            Ring r;
+            const uint32_t idesc = lm_idesc(a.rn);
+            bool ok = true;
+            int seg = 0;
+            for (int64_t u = u0; ok && u < u1; ++seg) {
+                const int j0 = static_cast<int>(u % J);
+                const int j1 = static_cast<int>(min(static_cast<int64_t>(J), j0 + (u1 - u)));
+                const int b = seg & 1;
+                if (seg >= 2 && !mbar_wait_bounded(&acc_empty[b], static_cast<uint32_t>(((seg >> 1) - 1) & 1), kLmTimeout))
+                    break;
+                tc_fence_after();
+                for (int j = j0; j < j1; ++j) {
+                    ok = mbar_wait_bounded(&full[r.slot], static_cast<uint32_t>(r.phase), kLmTimeout);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t sa = smem_addr(ring) + r.slot * stage_bytes;
+#pragma unroll
+                    for (int k = 0; k < kLmSlab / 16; ++k)
+                        mma_bf16(tmem + b * (cols / 2), smem_desc_sw128(sa + 32u * k),
+                                 smem_desc_sw128(sa + kLmSlabBytes + 32u * k), idesc, (j != j0 || k != 0) ? 1u : 0u);
+                    mma_commit(&empty[r.slot]);
+                    r.next(S);
+                }
+                if (!ok) break;
+                mma_commit(&acc_full[b]);
+                u += j1 - j0;
+            }
+            if (works)
+                mma_commit(&done);
+            else
+                mbar_arrive(&done);
+        }
+        __syncwarp();
+    } else if (warp >= 4) {
+        const int quad = warp & 3, half = (warp - 4) >> 2, row = 32 * quad + lane;
+        int seg = 0;
+        for (int64_t u = u0; u < u1; ++seg) {
+            const int tile = static_cast<int>(u / J), j0 = static_cast<int>(u % J);
+            const int j1 = static_cast<int>(min(static_cast<int64_t>(J), j0 + (u1 - u)));
+            const int b = seg & 1;
+            const int adapter = a.tiles[tile].adapter;
+            const float scale = a.scales != nullptr ? a.scales[adapter] : 1.0f;
+            // the CTAs that share the tile: the last c with U c / G <= u, for its first and last slab
+            const int64_t first = static_cast<int64_t>(tile) * J;
+            const int c0 = static_cast<int>(((first + 1) * G - 1) / U), c1 = static_cast<int>(((first + J) * G - 1) / U);
+            // a wait that ran out ends all eight warps together: they share barriers
+            const bool ok = mbar_wait_bounded(&acc_full[b], static_cast<uint32_t>((seg >> 1) & 1), kLmTimeout);
+            if (!named_bar_and(1, kLmEpiWarps * 32, ok)) break;
+            tc_fence_after();
+            const uint32_t acc = tmem + b * (cols / 2) + (static_cast<uint32_t>(32 * quad) << 16);
+            float* mine = a.part + (static_cast<size_t>(blockIdx.x) + tile) * a.R * kLmTile + row;
+            for (int gi = half; gi < a.rn / 16; gi += 2) {
+                float v[16];
+                tmem_ld16(acc + 16 * gi, v);
+                if (c0 == c1) {
+                    lm_write_v(a, tile, gi, row, scale, v);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        if (16 * gi + i < a.R) mine[(16 * gi + i) * kLmTile] = v[i];
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&acc_empty[b]);
+            if (c0 != c1) {
+                __threadfence();
+                named_bar_sync(1, kLmEpiWarps * 32);
+                if (warp == 4 && lane == 0) {
+                    s_last = atomicAdd(&a.arrived[tile], 1) == c1 - c0;
+                    __threadfence();
+                }
+                named_bar_sync(1, kLmEpiWarps * 32);
+                if (s_last) {
+                    for (int gi = half; gi < a.rn / 16; gi += 2) {
+                        float v[16];
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) v[i] = 0.0f;
+                        for (int c = c0; c <= c1; ++c) {
+                            const float* p = a.part + (static_cast<size_t>(c) + tile) * a.R * kLmTile + row;
+                            float w[16];
+#pragma unroll
+                            for (int i = 0; i < 16; ++i)
+                                w[i] = 16 * gi + i < a.R ? __ldcg(p + (16 * gi + i) * kLmTile) : 0.0f;
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) v[i] += w[i];
+                        }
+                        lm_write_v(a, tile, gi, row, scale, v);
+                    }
+                }
+            }
+            u += j1 - j0;       // s_last is set again only behind the next tile's first barrier
+        }
+    }
+    mbar_wait_bounded(&done, 0u, kLmTimeout);
+    __syncthreads();
+    if (threadIdx.x == 0) lm_drain(full, S, s_issued);
+    tc_fence_after();
+    __syncthreads();
+    if (warp == 0) tmem_dealloc(tmem, cols);
+}
+
+template <typename O>
+__global__ void __launch_bounds__(kLmThreads) lora_expand_kernel(const __grid_constant__ CUtensorMap vmap,
+                                                                 const __grid_constant__ CUtensorMap bmap,
+                                                                 const __grid_constant__ CUtensorMap basemap,
+                                                                 const LmArgs a) {
+    constexpr int kSubCols = 128 / sizeof(O);          // columns of a 128-byte row piece
+    constexpr int kSubs = kLmCols / kSubCols;
+    extern __shared__ uint8_t lm_raw[];
+    const uint32_t raw = smem_addr(lm_raw);
+    uint8_t* sv = lm_raw + (((raw + 1023u) & ~1023u) - raw);
+    const int v_slabs = a.parts * a.ks;
+    uint8_t* sb = sv + static_cast<size_t>(a.v_bufs) * v_slabs * kLmSlabBytes;
+    uint8_t* sbase = sb + static_cast<size_t>(a.b_stages) * kLmSlabBytes;
+    __shared__ __align__(8) uint64_t v_full[2], v_empty[2], b_full[kLmMaxStages], b_empty[kLmMaxStages],
+        base_full[kLmMaxStages], base_empty[kLmMaxStages], acc_full[2], acc_empty[2], done;
+    __shared__ uint32_t s_tmem;
+    __shared__ int s_issued[3];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    constexpr uint32_t kCols = 2 * kLmCols;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&v_full[i], 1);
+            mbar_init(&v_empty[i], 1);
+            mbar_init(&acc_full[i], 1);
+            mbar_init(&acc_empty[i], kLmEpiWarps);
+        }
+        for (int i = 0; i < a.b_stages; ++i) {
+            mbar_init(&b_full[i], 1);
+            mbar_init(&b_empty[i], 1);
+        }
+        for (int i = 0; i < a.base_stages; ++i) {
+            mbar_init(&base_full[i], 1);
+            mbar_init(&base_empty[i], kLmEpiWarps / 2);
+        }
+        mbar_init(&done, 1);
+        s_issued[0] = s_issued[1] = s_issued[2] = 0;
+        fence_mbar_init();
+    }
+    if (warp == 0) {
+        tmem_alloc(&s_tmem, kCols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = s_tmem;
+    griddep_wait();
+    griddep_launch();
+
+    const int C = (a.N + kLmCols - 1) / kLmCols;
+    const int64_t U = static_cast<int64_t>(*a.ntiles) * C, G = gridDim.x;   // a CTA may get no item
+    const int64_t u0 = U * blockIdx.x / G, u1 = U * (blockIdx.x + 1) / G;
+
+    if (warp == 0) {
+        Ring rv, rb, rx;
+        int nv = 0, nb = 0, nx = 0;
+        bool ok = true;
+        int cur = -1;
+        LmTile t{};
+        int4 rows = make_int4(0, 0, 0, 0);
+        for (int64_t u = u0; u < u1; ++u) {
+            const int tile = static_cast<int>(u / C), n0 = static_cast<int>(u % C) * kLmCols;
+            if (tile != cur) {
+                cur = tile;
+                t = a.tiles[tile];
+                rows = lm_rows(a, t, lane);
+                ok = nv < a.v_bufs || mbar_wait_bounded(&v_empty[rv.slot], static_cast<uint32_t>(rv.phase ^ 1), kLmTimeout);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(&v_full[rv.slot], static_cast<uint32_t>(v_slabs * kLmSlabBytes));
+                    for (int i = 0; i < v_slabs; ++i)
+                        tma_load_2d(smem_addr(sv + static_cast<size_t>(rv.slot * v_slabs + i) * kLmSlabBytes), &vmap, 0,
+                                    (tile * v_slabs + i) * kLmTile, &v_full[rv.slot]);
+                }
+                __syncwarp();
+                ++nv;
+                rv.next(a.v_bufs);
+            }
+            for (int s = 0; s < a.ks; ++s) {
+                ok = nb < a.b_stages || mbar_wait_bounded(&b_empty[rb.slot], static_cast<uint32_t>(rb.phase ^ 1), kLmTimeout);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(&b_full[rb.slot], kLmSlabBytes);
+                    tma_load_2d(smem_addr(sb + static_cast<size_t>(rb.slot) * kLmSlabBytes), &bmap, s * kLmSlab,
+                                t.adapter * a.N + n0, &b_full[rb.slot]);
+                }
+                __syncwarp();
+                ++nb;
+                rb.next(a.b_stages);
+            }
+            if (!ok) break;
+            const int quads = (t.count + 3) / 4;
+            for (int s = 0; s < kSubs && n0 + s * kSubCols < a.N; ++s) {
+                ok = nx < a.base_stages ||
+                     mbar_wait_bounded(&base_empty[rx.slot], static_cast<uint32_t>(rx.phase ^ 1), kLmTimeout);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                if (lane == 0) mbar_arrive_expect_tx(&base_full[rx.slot], static_cast<uint32_t>(quads * 512));
+                __syncwarp();
+                if (lane < quads)
+                    tma_gather4(smem_addr(sbase + static_cast<size_t>(rx.slot) * kLmSlabBytes) + 512 * lane, &basemap,
+                                n0 + s * kSubCols, rows, &base_full[rx.slot]);
+                ++nx;
+                rx.next(a.base_stages);
+            }
+            if (!ok) break;
+        }
+        if (lane == 0) s_issued[0] = nv, s_issued[1] = nb, s_issued[2] = nx;
+        __syncwarp();
+    } else if (warp == 1) {
+        if (lane == 0) {
+            Ring rv, rb;
+            const uint32_t idesc = lm_idesc(kLmCols);
+            bool ok = true;
+            int cur = -1, i = 0;
+            uint32_t v = 0;
+            for (int64_t u = u0; u < u1; ++u, ++i) {
+                const int tile = static_cast<int>(u / C);
+                const int b = i & 1;
+                if (i >= 2 && !mbar_wait_bounded(&acc_empty[b], static_cast<uint32_t>(((i >> 1) - 1) & 1), kLmTimeout)) break;
+                if (tile != cur) {
+                    cur = tile;
+                    if (!mbar_wait_bounded(&v_full[rv.slot], static_cast<uint32_t>(rv.phase), kLmTimeout)) break;
+                    v = smem_addr(sv) + rv.slot * v_slabs * kLmSlabBytes;
+                }
+                tc_fence_after();
+                uint32_t more = 0u;
+                for (int s = 0; s < a.ks; ++s) {
+                    ok = mbar_wait_bounded(&b_full[rb.slot], static_cast<uint32_t>(rb.phase), kLmTimeout);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t sbs = smem_addr(sb) + rb.slot * kLmSlabBytes;
+                    const int steps = (min(a.R - s * kLmSlab, kLmSlab) + 15) / 16;
+                    for (int p = 0; p < a.parts; ++p)
+                        for (int k = 0; k < steps; ++k) {
+                            mma_bf16(tmem + b * kLmCols, smem_desc_sw128(v + (p * a.ks + s) * kLmSlabBytes + 32u * k),
+                                     smem_desc_sw128(sbs + 32u * k), idesc, more);
+                            more = 1u;
+                        }
+                    mma_commit(&b_empty[rb.slot]);
+                    rb.next(a.b_stages);
+                }
+                if (!ok) break;
+                mma_commit(&acc_full[b]);
+                if (u + 1 == u1 || static_cast<int>((u + 1) / C) != tile) {
+                    mma_commit(&v_empty[rv.slot]);
+                    rv.next(a.v_bufs);
+                }
+            }
+            if (u0 < u1)
+                mma_commit(&done);
+            else
+                mbar_arrive(&done);
+        }
+        __syncwarp();
+    } else if (warp < 4) {
+        // rows of tokens without an adapter
+        if (a.out != a.base) {
+            const size_t row_bytes = static_cast<size_t>(a.N) * sizeof(O);
+            for (int t0 = (blockIdx.x * 2 + warp - 2) * 32; t0 < a.T; t0 += gridDim.x * 64) {
+                uint32_t none = __ballot_sync(0xffffffffu, t0 + lane < a.T && a.row_idx[min(t0 + lane, a.T - 1)] < 0);
+                for (; none != 0; none &= none - 1) {
+                    const size_t at = static_cast<size_t>(t0 + __ffs(none) - 1) * row_bytes;
+                    const uint8_t* src = static_cast<const uint8_t*>(a.base) + at;
+                    uint8_t* dst = static_cast<uint8_t*>(a.out) + at;
+#pragma unroll 8
+                    for (size_t i = lane * 16; i < row_bytes; i += 512) st_v4(dst + i, ld_nc_v4(src + i));
+                }
+            }
+        }
+    } else {
+        const int quad = warp & 3, grp = (warp - 4) >> 2, row = 32 * quad + lane;
+        Ring rx;
+        int cur = -1, i = 0, count = 0;
+        int32_t token[8];          // of rows 32 quad + 4 it + lane / 8, which this lane writes a piece of
+        for (int64_t u = u0; u < u1; ++u, ++i) {
+            const int tile = static_cast<int>(u / C), n0 = static_cast<int>(u % C) * kLmCols;
+            const int b = i & 1;
+            if (tile != cur) {
+                cur = tile;
+                const LmTile t = a.tiles[tile];
+                count = t.count;
+#pragma unroll
+                for (int it = 0; it < 8; ++it) {
+                    const int r = 32 * quad + 4 * it + (lane >> 3);
+                    token[it] = r < count ? a.row_token[t.row0 + r] : 0;
+                }
+            }
+            bool ok = mbar_wait_bounded(&acc_full[b], static_cast<uint32_t>((i >> 1) & 1), kLmTimeout);
+            tc_fence_after();
+            const uint32_t acc = tmem + b * kLmCols + (static_cast<uint32_t>(32 * quad) << 16);
+            for (int s = 0; s < kSubs && n0 + s * kSubCols < a.N; ++s, rx.next(a.base_stages)) {
+                if ((s & 1) != grp) continue;
+                ok = mbar_wait_bounded(&base_full[rx.slot], static_cast<uint32_t>(rx.phase), kLmTimeout) && ok;
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                const uint32_t tile_s = smem_addr(sbase) + rx.slot * kLmSlabBytes;
+                const uint32_t mine = tile_s + row * 128;
+#pragma unroll
+                for (int h = 0; h < kSubCols / 32; ++h) {
+                    float d[32];
+                    tmem_ld32(acc + s * kSubCols + 32 * h, d);
+                    if constexpr (sizeof(O) == 4) {
+#pragma unroll
+                        for (int c = 0; c < 8; ++c) {
+                            const uint32_t at = mine + ((c ^ (row & 7)) << 4);
+                            const uint4 w = lds128(at);
+                            const float2 lo = add2(make_float2(__uint_as_float(w.x), __uint_as_float(w.y)),
+                                                   make_float2(d[4 * c], d[4 * c + 1]));
+                            const float2 hi = add2(make_float2(__uint_as_float(w.z), __uint_as_float(w.w)),
+                                                   make_float2(d[4 * c + 2], d[4 * c + 3]));
+                            sts128(at, make_uint4(__float_as_uint(lo.x), __float_as_uint(lo.y), __float_as_uint(hi.x),
+                                                  __float_as_uint(hi.y)));
+                        }
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            const uint32_t at = mine + (((4 * h + c) ^ (row & 7)) << 4);
+                            uint4 w = lds128(at);
+                            w.x = pack_bf16x2_rn(add2(unpack_bf16x2(w.x), make_float2(d[8 * c], d[8 * c + 1])));
+                            w.y = pack_bf16x2_rn(add2(unpack_bf16x2(w.y), make_float2(d[8 * c + 2], d[8 * c + 3])));
+                            w.z = pack_bf16x2_rn(add2(unpack_bf16x2(w.z), make_float2(d[8 * c + 4], d[8 * c + 5])));
+                            w.w = pack_bf16x2_rn(add2(unpack_bf16x2(w.w), make_float2(d[8 * c + 6], d[8 * c + 7])));
+                            sts128(at, w);
+                        }
+                    }
+                }
+                __syncwarp();
+                const int chunk = lane & 7, col = n0 + s * kSubCols + chunk * (16 / static_cast<int>(sizeof(O)));
+#pragma unroll
+                for (int it = 0; it < 8; ++it) {
+                    const int r = 32 * quad + 4 * it + (lane >> 3);
+                    const uint4 w = lds128(tile_s + r * 128 + ((chunk ^ (r & 7)) << 4));
+                    if (r < count && col < a.N)
+                        st_v4(static_cast<O*>(a.out) + static_cast<size_t>(token[it]) * a.N + col, w);
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&base_empty[rx.slot]);
+            }
+            if (!__all_sync(0xffffffffu, ok)) break;
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&acc_empty[b]);
+        }
+    }
+    mbar_wait_bounded(&done, 0u, kLmTimeout);
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        lm_drain(v_full, a.v_bufs, s_issued[0]);
+        lm_drain(b_full, a.b_stages, s_issued[1]);
+        lm_drain(base_full, a.base_stages, s_issued[2]);
+    }
+    tc_fence_after();
+    __syncthreads();
+    if (warp == 0) tmem_dealloc(tmem, kCols);
+}
+
+int lm_most_tiles(int T, int L) { return (T + kLmTile - 1) / kLmTile + (L < T ? L : T); }
+int lm_parts(bool bf16) { return bf16 ? 2 : 3; }
+size_t lm_pad(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
+
+// The workspace of the many-token path, in order; `base` NULL only sizes it.
+struct LmLayout {
+    size_t offsets, row_idx, row_token, dispatch, tiles, ntiles, arrived, part, v, bytes;
+};
+LmLayout lm_layout(int T, int H, int R, int L) {
+    LmLayout l;
+    const size_t nt = static_cast<size_t>(lm_most_tiles(T, L)), ks = static_cast<size_t>((R + kLmSlab - 1) / kLmSlab);
+    size_t at = 0;
+    auto take = [&](size_t n) {
+        const size_t p = at;
+        at += lm_pad(n);
+        return p;
+    };
+    l.offsets = take((static_cast<size_t>(L) + 1) * 4);
+    l.row_idx = take(static_cast<size_t>(T) * 4);
+    l.row_token = take(static_cast<size_t>(T) * 4);
+    l.dispatch = take(dispatch_workspace_bytes(T, L));
+    l.tiles = take(nt * sizeof(LmTile));
+    l.ntiles = take(4);
+    l.arrived = take(nt * 4);
+    l.part = take((nt + static_cast<size_t>(device_info().sm_count)) * R * kLmTile * 4);
+    l.v = take(nt * 3 * ks * kLmSlabBytes);
+    l.bytes = at;
+    return l;
+}
+
+cudaError_t lm_launch(const void* kernel, int grid, int threads, size_t smem, void** args, cudaStream_t s) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelExC(&cfg, kernel, args);
+}
+
+cudaError_t launch_lora_many(const LoraLaunch& l, cudaStream_t s) {
+    const LmLayout at = lm_layout(l.T, l.H, l.R, l.L);
+    uint8_t* w = static_cast<uint8_t*>(l.workspace);
+    LmArgs a{};
+    int32_t* offsets = reinterpret_cast<int32_t*>(w + at.offsets);
+    int32_t* row_idx = reinterpret_cast<int32_t*>(w + at.row_idx);
+    int32_t* row_token = reinterpret_cast<int32_t*>(w + at.row_token);
+    a.offsets = offsets, a.row_idx = row_idx, a.row_token = row_token;
+    a.tiles = reinterpret_cast<LmTile*>(w + at.tiles);
+    a.ntiles = reinterpret_cast<int32_t*>(w + at.ntiles);
+    a.arrived = reinterpret_cast<int32_t*>(w + at.arrived);
+    a.part = reinterpret_cast<float*>(w + at.part);
+    a.v = reinterpret_cast<uint16_t*>(w + at.v);
+    a.scales = l.scales, a.base = l.base, a.out = l.out;
+    a.T = l.T, a.H = l.H, a.N = l.N, a.R = l.R, a.L = l.L;
+    a.rn = (l.R + 15) / 16 * 16;
+    a.ks = (l.R + kLmSlab - 1) / kLmSlab;
+    a.parts = lm_parts(l.bf16);
+    a.stages = kLmBytes / (kLmSlabBytes + a.rn * 128);
+    if (a.stages > kLmMaxStages) a.stages = kLmMaxStages;
+    // the expand kernel's 13 slabs of 16 KB: v (twice while it is one slab wide), B, and the rest base
+    a.v_bufs = a.ks == 1 ? 2 : 1;
+    a.b_stages = a.ks == 1 ? 2 : 3;
+    a.base_stages = kLmBytes / kLmSlabBytes - a.v_bufs * a.parts * a.ks - a.b_stages;
+    CUtensorMap xmap, amap, vmap, bmap, basemap;
+    constexpr auto kBf16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    constexpr auto kSw = CU_TENSOR_MAP_SWIZZLE_128B;
+    const uint64_t v_rows = static_cast<uint64_t>(lm_most_tiles(l.T, l.L)) * a.parts * a.ks * kLmTile;
+    if (!encode_2d_map(&xmap, kBf16, 2, l.x, l.T, l.H, static_cast<uint64_t>(l.H) * 2, 1, kLmSlab, kSw) ||
+        !encode_2d_map(&amap, kBf16, 2, l.a, static_cast<uint64_t>(l.L) * l.R, l.H, static_cast<uint64_t>(l.H) * 2,
+                       static_cast<uint32_t>(a.rn), kLmSlab, kSw) ||
+        !encode_2d_map(&vmap, kBf16, 2, a.v, v_rows, kLmSlab, kLmSlab * 2, kLmTile, kLmSlab, kSw) ||
+        !encode_2d_map(&bmap, kBf16, 2, l.b, static_cast<uint64_t>(l.L) * l.N, l.R, static_cast<uint64_t>(l.R) * 2,
+                       kLmCols, kLmSlab, kSw) ||
+        !encode_2d_map(&basemap, l.bf16 ? kBf16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, l.bf16 ? 2 : 4, l.base, l.T, l.N,
+                       static_cast<uint64_t>(l.N) * (l.bf16 ? 2 : 4), 1, l.bf16 ? 64 : 32, kSw))
+        return cudaErrorInvalidValue;
+    cudaError_t e = launch_dispatch(l.ids, l.T, 1, 0, l.L, offsets, row_idx, row_token, w + at.dispatch, s);
+    if (e != cudaSuccess) return e;
+    void* targs[] = {&a};
+    e = lm_launch(reinterpret_cast<const void*>(lora_tiles_kernel), 1, 1024, 0, targs, s);
+    if (e != cudaSuccess) return e;
+    const int smem = kLmBytes + 1024;
+    const void* shrink = reinterpret_cast<const void*>(lora_shrink_kernel);
+    const void* expand = l.bf16 ? reinterpret_cast<const void*>(lora_expand_kernel<uint16_t>)
+                                : reinterpret_cast<const void*>(lora_expand_kernel<float>);
+    for (const void* k : {shrink, expand}) {
+        e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
+    }
+    void* sargs[] = {&xmap, &amap, &a};
+    e = lm_launch(shrink, device_info().sm_count, kLmThreads, smem, sargs, s);
+    if (e != cudaSuccess) return e;
+    void* eargs[] = {&vmap, &bmap, &basemap, &a};
+    return lm_launch(expand, device_info().sm_count, kLmThreads, smem, eargs, s);
+}
+
 }  // namespace
 
 size_t lora_workspace_bytes(int T, int H, int N, int R, int L) {
-    const int n = T < kLoraThreads ? T : kLoraThreads;
-    return static_cast<size_t>(lora_splits(n, H)) * n * R * sizeof(float);
+    if (T > kLoraThreads) return lm_layout(T, H, R, L).bytes;
+    return static_cast<size_t>(lora_splits(T, H)) * T * R * sizeof(float);
 }
 
 cudaError_t launch_lora_add(const LoraLaunch& l, cudaStream_t s) {
-    const size_t size = l.bf16 ? 2 : 4;
-    for (int t0 = 0; t0 < l.T; t0 += kLoraThreads) {
-        LoraArgs a{};
-        a.T = l.T - t0 < kLoraThreads ? l.T - t0 : kLoraThreads;
-        a.H = l.H, a.N = l.N, a.R = l.R, a.L = l.L;
-        a.x = l.x + static_cast<size_t>(t0) * l.H;
-        a.a = l.a, a.b = l.b, a.scales = l.scales;
-        a.ids = l.ids + t0;
-        a.base = static_cast<const uint8_t*>(l.base) + static_cast<size_t>(t0) * l.N * size;
-        a.out = static_cast<uint8_t*>(l.out) + static_cast<size_t>(t0) * l.N * size;
-        a.part = static_cast<float*>(l.workspace);
-        a.splits = lora_splits(l.T < kLoraThreads ? l.T : kLoraThreads, l.H);
-        a.kc = ((l.H + a.splits - 1) / a.splits + 31) / 32 * 32;
-        a.splits = (l.H + a.kc - 1) / a.kc;
-        const dim3 grid(a.T, a.splits);
-        cudaError_t e;
-        if (l.R <= 16)
-            e = lora_launch(lora_shrink_few_kernel<1>, grid, kLoraThreads, a, s);
-        else if (l.R <= 32)
-            e = lora_launch(lora_shrink_few_kernel<2>, grid, kLoraThreads, a, s);
-        else if (l.R <= 64)
-            e = lora_launch(lora_shrink_few_kernel<4>, grid, kLoraThreads, a, s);
-        else
-            e = lora_launch(lora_shrink_few_kernel<8>, grid, kLoraThreads, a, s);
-        if (e != cudaSuccess) return e;
-        const dim3 egrid(a.T, (l.N + kLoraExpCols - 1) / kLoraExpCols);
-        e = l.bf16 ? lora_launch(lora_expand_few_kernel<uint16_t>, egrid, kLoraExpThreads, a, s)
-                   : lora_launch(lora_expand_few_kernel<float>, egrid, kLoraExpThreads, a, s);
-        if (e != cudaSuccess) return e;
-    }
-    return cudaSuccess;
+    if (l.T > kLoraThreads) return launch_lora_many(l, s);
+    LoraArgs a{};
+    a.T = l.T, a.H = l.H, a.N = l.N, a.R = l.R, a.L = l.L;
+    a.x = l.x, a.a = l.a, a.b = l.b, a.ids = l.ids, a.scales = l.scales, a.base = l.base, a.out = l.out;
+    a.part = static_cast<float*>(l.workspace);
+    a.splits = lora_splits(l.T, l.H);
+    a.kc = ((l.H + a.splits - 1) / a.splits + 31) / 32 * 32;
+    a.splits = (l.H + a.kc - 1) / a.kc;
+    const dim3 grid(a.T, a.splits);
+    cudaError_t e;
+    if (l.R <= 16)
+        e = lora_launch(lora_shrink_few_kernel<1>, grid, kLoraThreads, a, s);
+    else if (l.R <= 32)
+        e = lora_launch(lora_shrink_few_kernel<2>, grid, kLoraThreads, a, s);
+    else if (l.R <= 64)
+        e = lora_launch(lora_shrink_few_kernel<4>, grid, kLoraThreads, a, s);
+    else
+        e = lora_launch(lora_shrink_few_kernel<8>, grid, kLoraThreads, a, s);
+    if (e != cudaSuccess) return e;
+    const dim3 egrid(a.T, (l.N + kLoraExpCols - 1) / kLoraExpCols);
+    return l.bf16 ? lora_launch(lora_expand_few_kernel<uint16_t>, egrid, kLoraExpThreads, a, s)
+                  : lora_launch(lora_expand_few_kernel<float>, egrid, kLoraExpThreads, a, s);
 }
 
 }  // namespace mb

@@ -75,32 +75,6 @@ struct RouterProjArgs {
     float scale;
 };
 
-// ---- tcgen05 MMA primitives (cta_group::1; tensor-memory helpers in tmem.cuh)
-// D[128 x N] (+)= A[128 x 16] B[N x 16]^T, BF16 operands from shared memory.
-__device__ __forceinline__ void mma_bf16(uint32_t tmem_d, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
-                                         uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, {%5, %6, %7, %8}, p;\n\t}" ::"r"(tmem_d),
-        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(0u), "r"(0u), "r"(0u), "r"(0u)
-        : "memory");
-}
-// Arrive on `bar` once every MMA this thread issued so far has completed.
-__device__ __forceinline__ void mma_commit(uint64_t* bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
-                     smem_addr(bar))
-                 : "memory");
-}
-// Shared-memory matrix descriptor, K-major, 128-byte swizzle: 8-row groups
-// 1024 bytes apart (stride byte offset), leading byte offset unused (1),
-// descriptor version 1, swizzle mode 2.
-__device__ __forceinline__ uint64_t smem_desc_sw128(uint32_t saddr) {
-    return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) | (static_cast<uint64_t>(1u) << 16) |
-           (static_cast<uint64_t>(1024u >> 4) << 32) | (static_cast<uint64_t>(1u) << 46) |
-           (static_cast<uint64_t>(2u) << 61);
-}
-
 template <int C, int NE>
 __global__ void __launch_bounds__(kRpThreads) router_proj_kernel(const __grid_constant__ CUtensorMap xmap,
                                                                  const __grid_constant__ CUtensorMap wmap,

@@ -542,7 +542,8 @@ const char* mb_last_error(void);
  * shared-memory slot ran out; bit 1: a drain wait ran out; bit 2: a
  * consumer's wait for a copied row ran out; bit 3: the router projection's
  * wait for its tensor-core MMAs ran out; bit 4: the finalize all-reduce's
- * wait for a peer's partial ran out.  0 means no kernel reported a
+ * wait for a peer's partial ran out; bit 5: a wait inside the low-rank adapters'
+ * tensor-core kernels ran out.  0 means no kernel reported a
  * timeout since the last call.  Returns -1 (and sets mb_last_error) when the
  * CUDA runtime fails.
  */
