@@ -26,17 +26,16 @@
 // is cut into tiles of 128 tokens, and both products run on the tensor cores
 // (tcgen05, accumulators in tensor memory), one persistent CTA per SM: a TMA
 // warp, an MMA thread and eight epilogue warps.
-//   shrink  All tiles' slabs of 64 k form one line that is cut into equal
+//   shrink  All tiles' steps of 128 k form one line that is cut into equal
 //     pieces, one per CTA, so the SMs finish together whatever the sizes of
-//     the groups.  The rows of a tile lie anywhere in x: 32 lanes fetch four
-//     each (gather4).  A tile that several CTAs share is summed by the one that
+//     the groups.  The rows of a tile lie anywhere in x: four warps fetch them
+//     in 16-byte pieces.  A tile that several CTAs share is summed by the one that
 //     arrives last, from the partials, in the CTAs' order (an integer counter
 //     per tile; the sum's order does not depend on the arrival).  It writes v
 //     scaled and split into BF16 parts (3 for FP32 outputs: 2^-24 of v is left;
 //     2 for BF16 outputs: 2^-16), in the layout of the next MMA's operand.
 //   expand  Work items are a tile x 128 columns, cut the same way.  D = sum
-//     over the parts v_p B^T; base arrives by gather4 in the swizzled layout in
-//     which an epilogue thread reads its row without bank conflicts, the sum
+//     over the parts v_p B^T; base arrives in the swizzled layout in which an epilogue thread reads its row without bank conflicts, the sum
 //     replaces it there, and the warp writes whole 128-byte rows of out.
 #include "internal.h"
 #include "common.cuh"
@@ -279,12 +278,17 @@ cudaError_t lora_launch(F* kernel, dim3 grid, int threads, const LoraArgs& a, cu
 // ------------------------------------------------------------------ many tokens
 constexpr int kLmTile = 128;                 // tokens per tile (M of the MMAs)
 constexpr int kLmSlab = 64;                  // k per slab: 128 bytes of BF16
+constexpr int kLmStep = 2;                   // slabs per ring stage of the shrink kernel
 constexpr int kLmSlabBytes = kLmTile * 128;  // 16 KB
 constexpr int kLmCols = 128;                 // columns of out per work item
-constexpr int kLmThreads = 12 * 32;          // TMA, MMA, two that copy rows without an adapter, 8 epilogue warps
+constexpr int kLmThreads = 16 * 32;          // TMA, MMA, 2 warps that copy rows without an adapter, 8 epilogue, 4 loading
+constexpr int kLmLoadWarp = 12;              // first of the warps that gather rows
+constexpr int kLmPlanTokens = 32768;         // most tokens and adapters the one-CTA plan takes
+constexpr int kLmPlanAdapters = 1024;
 constexpr int kLmEpiWarps = 8;
 constexpr int kLmBytes = 208 * 1024;         // ring buffers of a CTA
 constexpr int kLmMaxStages = 12;
+constexpr int kLmChain = 8;                  // steps (of 2 slabs) the shrink adds up in tensor memory, see below
 constexpr unsigned int kLmTimeout = 32u;     // bit 5 of the device status word
 
 struct LmTile {
@@ -292,14 +296,15 @@ struct LmTile {
 };
 
 struct LmArgs {
-    const int32_t* offsets;      // [L + 1] first row of each adapter's group
-    const int32_t* row_idx;      // [T] row of a token, -1: no adapter
-    const int32_t* row_token;    // [T] token of a row
+    const int32_t* ids;          // [T]
+    const int32_t* offsets;      // [L + 1] first row of each adapter's group (large plans only)
+    int32_t* row_token;          // [T] token of a row of the grouped order
     LmTile* tiles;
     int32_t* ntiles;             // [1]
     int32_t* arrived;            // [tiles] CTAs that have left their partial
     float* part;                 // [SMs + tiles][R][128]
     uint16_t* v;                 // [tiles][parts][ks][128][64]
+    const uint16_t* x;
     const float* scales;
     const void* base;
     void* out;
@@ -356,27 +361,116 @@ __global__ void __launch_bounds__(1024) lora_tiles_kernel(const LmArgs a) {
     }
 }
 
-// Four rows of a 2-D tensor, 128 bytes of each, to shared memory.
-__device__ __forceinline__ void tma_gather4(uint32_t dst, const void* tmap, int x, int4 r, uint64_t* bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
-        "l"(tmap), "r"(x), "r"(r.x), "r"(r.y), "r"(r.z), "r"(r.w), "r"(smem_addr(bar))
-        : "memory");
+// The whole plan in one CTA: a stable counting sort of the tokens by adapter
+// (so the rows' order, and with it every sum's, is the same run to run) and the
+// tiles.  Warp w takes the w-th run of tokens 32 at a time; the lanes of one
+// adapter find each other by a match, and the warp's running count of that
+// adapter gives their places.  8192 tokens: 4 us, against 12 us for the
+// general dispatch and the tiles kernel, which take the larger batches.
+__global__ void __launch_bounds__(1024) lora_plan_kernel(const LmArgs a) {
+    extern __shared__ __align__(16) uint8_t plan_raw[];
+    uint16_t* sid = reinterpret_cast<uint16_t*>(plan_raw);      // [T] adapter, 0xffff: none
+    uint16_t* cnt = sid + (a.T + 7) / 8 * 8;                    // [32][L]
+    __shared__ int2 s_warp[32];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    for (int i = tid; i < 32 * a.L; i += 1024) cnt[i] = 0;
+    griddep_wait();
+    griddep_launch();
+#pragma unroll 8
+    for (int i = tid; i < a.T; i += 1024) {
+        const int id = a.ids[i];
+        sid[i] = id >= 0 && id < a.L ? static_cast<uint16_t>(id) : static_cast<uint16_t>(0xffff);
+    }
+    __syncthreads();
+    const int span = (a.T + 1023) / 1024 * 32, lo = warp * span, hi = min(a.T, lo + span);
+    uint16_t* mine = cnt + warp * a.L;
+    for (int i0 = lo; i0 < hi; i0 += 32) {
+        const int e = i0 + lane < hi ? sid[i0 + lane] : 0xffff;
+        const uint32_t m = __match_any_sync(0xffffffffu, e);
+        if (e != 0xffff && (m & ((1u << lane) - 1u)) == 0) mine[e] = static_cast<uint16_t>(mine[e] + __popc(m));
+        __syncwarp();
+    }
+    __syncthreads();
+    int c[32], total = 0;       // the warps' counts of adapter `tid`
+#pragma unroll
+    for (int w = 0; w < 32; ++w) c[w] = tid < a.L ? cnt[w * a.L + tid] : 0;
+#pragma unroll
+    for (int w = 0; w < 32; ++w) total += c[w];
+    const int tiles = (total + kLmTile - 1) / kLmTile;
+    int2 scan = make_int2(total, tiles);
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const int p = __shfl_up_sync(0xffffffffu, scan.x, off), q = __shfl_up_sync(0xffffffffu, scan.y, off);
+        if (lane >= off) scan.x += p, scan.y += q;
+    }
+    if (lane == 31) s_warp[warp] = scan;
+    __syncthreads();
+    int row = scan.x - total, tile = scan.y - tiles, all = 0;
+    for (int w = 0; w < 32; ++w) {
+        if (w < warp) row += s_warp[w].x, tile += s_warp[w].y;
+        all += s_warp[w].y;
+    }
+    if (tid < a.L) {
+        for (int i = 0; i < tiles; ++i)
+            a.tiles[tile + i] = LmTile{tid, row + i * kLmTile, min(kLmTile, total - i * kLmTile), 0};
+        int at = row;
+#pragma unroll
+        for (int w = 0; w < 32; ++w) {
+            cnt[w * a.L + tid] = static_cast<uint16_t>(at);     // first row of this warp's tokens of the adapter
+            at += c[w];
+        }
+    }
+    if (tid == 0) *a.ntiles = all;
+    for (int i = tid; i < all; i += 1024) a.arrived[i] = 0;
+    __syncthreads();
+    for (int i0 = lo; i0 < hi; i0 += 32) {
+        const int e = i0 + lane < hi ? sid[i0 + lane] : 0xffff;
+        const uint32_t m = __match_any_sync(0xffffffffu, e);
+        const uint32_t below = m & ((1u << lane) - 1u);
+        const int first = e != 0xffff ? mine[e] : 0;
+        __syncwarp();
+        if (e != 0xffff) {
+            a.row_token[first + __popc(below)] = i0 + lane;
+            if (below == 0) mine[e] = static_cast<uint16_t>(first + __popc(m));
+        }
+        __syncwarp();
+    }
 }
 
-// The tokens of rows 4 lane .. 4 lane + 3 of a tile; rows behind its end
-// repeat the first (fetched, never used).
-__device__ __forceinline__ int4 lm_rows(const LmArgs& a, const LmTile& t, int lane) {
-    const int32_t* p = a.row_token + t.row0;
-    const int i = 4 * lane;
-    int4 r;
-    r.x = p[i < t.count ? i : 0];
-    r.y = p[i + 1 < t.count ? i + 1 : 0];
-    r.z = p[i + 2 < t.count ? i + 2 : 0];
-    r.w = p[i + 3 < t.count ? i + 3 : 0];
-    return r;
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool fetch) {   // else 16 zero bytes
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(fetch ? 16 : 0) : "memory");
 }
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+// Arrives on `bar` when this thread's copies so far have landed.
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+
+// A loading thread's share of a tile of 128 rows x 128 bytes: 16-byte piece
+// `tid % 8` of rows tid / 8 + 16 i, the 128-byte swizzle applied by hand.  (A
+// TMA gather of four such rows an instruction reached 1.6 TB/s here.)
+struct RowLoader {
+    int32_t token[8];
+    int count, r0, piece;
+    uint32_t at;
+    __device__ __forceinline__ RowLoader(int tid)
+        : count(0), r0(tid >> 3), piece(tid & 7),
+          at(static_cast<uint32_t>((tid >> 3) * 128 + (((tid & 7) ^ ((tid >> 3) & 7)) << 4))) {}
+    __device__ __forceinline__ void tile(const LmArgs& a, const LmTile& t) {
+        count = t.count;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) token[i] = r0 + 16 * i < count ? a.row_token[t.row0 + r0 + 16 * i] : 0;
+    }
+    // rows of `pitch` bytes, their bytes [byte0, byte0 + 128); past the pitch: zeros
+    __device__ __forceinline__ void load(uint32_t dst, const void* base, size_t pitch, size_t byte0) const {
+        const size_t b = byte0 + piece * 16;
+        const bool in = b < pitch;
+        const uint8_t* p = static_cast<const uint8_t*>(base) + (in ? b : 0);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (r0 + 16 * i < count) cp_async16(dst + at + 2048 * i, p + token[i] * pitch, in);
+    }
+};
 
 __device__ __forceinline__ uint32_t lm_idesc(int n) {   // FP32 += BF16 x BF16, both K-major, M = 128
     return (1u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(n >> 3) << 17) |
@@ -418,21 +512,28 @@ __device__ __forceinline__ void lm_write_v(const LmArgs& a, int tile, int gi, in
     }
 }
 
-__global__ void __launch_bounds__(kLmThreads) lora_shrink_kernel(const __grid_constant__ CUtensorMap xmap,
-                                                                 const __grid_constant__ CUtensorMap amap,
+// The tensor core cuts off what its FP32 accumulator cannot hold, always
+// towards zero, so a long chain of MMAs drifts (512 of them, H = 8192: 1.7e-6 of
+// the result in the mean).  After kLmChain steps (64 MMAs) the accumulator is
+// added to registers with ordinary rounding: 6e-7.  GH: groups of 16 ranks of
+// an epilogue thread (the eight warps halve the ranks).
+template <int GH>
+__global__ void __launch_bounds__(kLmThreads, 1) lora_shrink_kernel(const __grid_constant__ CUtensorMap amap,
                                                                  const LmArgs a) {
     extern __shared__ uint8_t lm_raw[];
     const uint32_t raw = smem_addr(lm_raw);
     uint8_t* ring = lm_raw + (((raw + 1023u) & ~1023u) - raw);
-    __shared__ __align__(8) uint64_t full[kLmMaxStages], empty[kLmMaxStages], acc_full[2], acc_empty[2], done;
+    __shared__ __align__(8) uint64_t x_full[kLmMaxStages], a_full[kLmMaxStages], empty[kLmMaxStages], acc_full[2],
+        acc_empty[2], done;
     __shared__ uint32_t s_tmem;
     __shared__ int s_issued, s_last;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int S = a.stages, stage_bytes = kLmSlabBytes + a.rn * 128;
+    const int S = a.stages, a_bytes = a.rn * 128, stage_bytes = kLmStep * (kLmSlabBytes + a_bytes);
     const uint32_t cols = a.rn <= 16 ? 32u : a.rn <= 32 ? 64u : a.rn <= 64 ? 128u : 256u;   // two accumulators
     if (threadIdx.x == 0) {
         for (int i = 0; i < S; ++i) {
-            mbar_init(&full[i], 1);
+            mbar_init(&x_full[i], 128);
+            mbar_init(&a_full[i], 1);
             mbar_init(&empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -454,39 +555,57 @@ __global__ void __launch_bounds__(kLmThreads) lora_shrink_kernel(const __grid_co
     griddep_wait();
     griddep_launch();
 
-    const int J = (a.H + kLmSlab - 1) / kLmSlab;
+    const int J = (a.H + kLmStep * kLmSlab - 1) / (kLmStep * kLmSlab);   // steps of a tile
     const int64_t U = static_cast<int64_t>(*a.ntiles) * J, G = min(static_cast<int64_t>(gridDim.x), U);
-    const bool works = blockIdx.x < G;       // every working CTA has at least one slab
+    const bool works = blockIdx.x < G;       // every working CTA has at least one step
     const int64_t u0 = works ? U * blockIdx.x / G : 0, u1 = works ? U * (blockIdx.x + 1) / G : 0;
 
     if (warp == 0) {
+        if (lane == 0) {
+            Ring r;
+            int issued = 0, j = static_cast<int>(u0 % J), tile = static_cast<int>(u0 / J);
+            int arow = u0 < u1 ? a.tiles[tile].adapter * a.R : 0;
+            for (int64_t u = u0; u < u1; ++u, ++j) {
+                if (j == J) {
+                    j = 0;
+                    arow = a.tiles[++tile].adapter * a.R;
+                }
+                if (issued >= S && !mbar_wait_bounded(&empty[r.slot], static_cast<uint32_t>(r.phase ^ 1), kLmTimeout)) break;
+                mbar_arrive_expect_tx(&a_full[r.slot], static_cast<uint32_t>(kLmStep * a_bytes));
+#pragma unroll
+                for (int h = 0; h < kLmStep; ++h)
+                    tma_load_2d(smem_addr(ring) + r.slot * stage_bytes + kLmStep * kLmSlabBytes + h * a_bytes, &amap,
+                                (j * kLmStep + h) * kLmSlab, arow, &a_full[r.slot]);
+                ++issued;
+                r.next(S);
+            }
+            s_issued = issued;
+        }
+        __syncwarp();
+    } else if (warp >= kLmLoadWarp) {
+        RowLoader rows(threadIdx.x - kLmLoadWarp * 32);
         Ring r;
         int issued = 0;
         bool ok = true;
+        const size_t pitch = static_cast<size_t>(a.H) * 2;
         for (int64_t u = u0; ok && u < u1;) {
-            const int tile = static_cast<int>(u / J), j0 = static_cast<int>(u % J);
-            const int j1 = static_cast<int>(min(static_cast<int64_t>(J), j0 + (u1 - u)));
-            const LmTile t = a.tiles[tile];
-            const int4 rows = lm_rows(a, t, lane);
-            const int quads = (t.count + 3) / 4;
+            const int j0 = static_cast<int>(u % J), j1 = static_cast<int>(min(static_cast<int64_t>(J), j0 + (u1 - u)));
+            rows.tile(a, a.tiles[u / J]);
             for (int j = j0; j < j1; ++j) {
                 ok = issued < S || mbar_wait_bounded(&empty[r.slot], static_cast<uint32_t>(r.phase ^ 1), kLmTimeout);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
-                uint8_t* st = ring + static_cast<size_t>(r.slot) * stage_bytes;
-                if (lane == 0)
-                    mbar_arrive_expect_tx(&full[r.slot], static_cast<uint32_t>(quads * 512 + a.rn * 128));
-                __syncwarp();
-                if (lane < quads) tma_gather4(smem_addr(st) + 512 * lane, &xmap, j * kLmSlab, rows, &full[r.slot]);
-                if (lane == 0)
-                    tma_load_2d(smem_addr(st + kLmSlabBytes), &amap, j * kLmSlab, t.adapter * a.R, &full[r.slot]);
+#pragma unroll
+                for (int h = 0; h < kLmStep; ++h)
+                    rows.load(smem_addr(ring) + r.slot * stage_bytes + h * kLmSlabBytes, a.x, pitch,
+                              static_cast<size_t>(j * kLmStep + h) * 128);
+                cp_async_arrive(&x_full[r.slot]);
                 ++issued;
                 r.next(S);
             }
             u += j1 - j0;
         }
-        if (lane == 0) s_issued = issued;
-        __syncwarp();
+        cp_async_wait_all();
     } else if (warp == 1) {
         if (lane == 0) {
             Ring r;
@@ -495,20 +614,27 @@ __global__ void __launch_bounds__(kLmThreads) lora_shrink_kernel(const __grid_co
             int seg = 0;
             for (int64_t u = u0; ok && u < u1; ++seg) {
                 const int j0 = static_cast<int>(u % J);
-                const int j1 = static_cast<int>(min(static_cast<int64_t>(J), j0 + (u1 - u)));
+                const int j1 = static_cast<int>(min(static_cast<int64_t>(min(J, j0 + kLmChain)), j0 + (u1 - u)));
                 const int b = seg & 1;
                 if (seg >= 2 && !mbar_wait_bounded(&acc_empty[b], static_cast<uint32_t>(((seg >> 1) - 1) & 1), kLmTimeout))
                     break;
                 tc_fence_after();
                 for (int j = j0; j < j1; ++j) {
-                    ok = mbar_wait_bounded(&full[r.slot], static_cast<uint32_t>(r.phase), kLmTimeout);
+                    ok = mbar_wait_bounded(&a_full[r.slot], static_cast<uint32_t>(r.phase), kLmTimeout) &&
+                         mbar_wait_bounded(&x_full[r.slot], static_cast<uint32_t>(r.phase), kLmTimeout);
                     if (!ok) break;
+                    // the rows were written through the generic proxy, by copies that the barrier has seen land;
+                    // the MMA reads through the async proxy
+                    fence_proxy_async_smem();
                     tc_fence_after();
-                    const uint32_t sa = smem_addr(ring) + r.slot * stage_bytes;
+                    const uint32_t sx = smem_addr(ring) + r.slot * stage_bytes, sa = sx + kLmStep * kLmSlabBytes;
 #pragma unroll
-                    for (int k = 0; k < kLmSlab / 16; ++k)
-                        mma_bf16(tmem + b * (cols / 2), smem_desc_sw128(sa + 32u * k),
-                                 smem_desc_sw128(sa + kLmSlabBytes + 32u * k), idesc, (j != j0 || k != 0) ? 1u : 0u);
+                    for (int h = 0; h < kLmStep; ++h)
+#pragma unroll
+                        for (int k = 0; k < kLmSlab / 16; ++k)
+                            mma_bf16(tmem + b * (cols / 2), smem_desc_sw128(sx + h * kLmSlabBytes + 32u * k),
+                                     smem_desc_sw128(sa + h * a_bytes + 32u * k), idesc,
+                                     (j != j0 || h != 0 || k != 0) ? 1u : 0u);
                     mma_commit(&empty[r.slot]);
                     r.next(S);
                 }
@@ -525,35 +651,52 @@ __global__ void __launch_bounds__(kLmThreads) lora_shrink_kernel(const __grid_co
     } else if (warp >= 4) {
         const int quad = warp & 3, half = (warp - 4) >> 2, row = 32 * quad + lane;
         int seg = 0;
-        for (int64_t u = u0; u < u1; ++seg) {
+        for (int64_t u = u0; u < u1;) {
             const int tile = static_cast<int>(u / J), j0 = static_cast<int>(u % J);
             const int j1 = static_cast<int>(min(static_cast<int64_t>(J), j0 + (u1 - u)));
-            const int b = seg & 1;
             const int adapter = a.tiles[tile].adapter;
             const float scale = a.scales != nullptr ? a.scales[adapter] : 1.0f;
             // the CTAs that share the tile: the last c with U c / G <= u, for its first and last slab
             const int64_t first = static_cast<int64_t>(tile) * J;
             const int c0 = static_cast<int>(((first + 1) * G - 1) / U), c1 = static_cast<int>(((first + J) * G - 1) / U);
+            float v[GH][16];
+#pragma unroll
+            for (int g = 0; g < GH; ++g)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) v[g][i] = 0.0f;
+            bool ok = true;
+            for (int j = j0; j < j1; j += kLmChain, ++seg) {
+                const int b = seg & 1;
+                ok = mbar_wait_bounded(&acc_full[b], static_cast<uint32_t>((seg >> 1) & 1), kLmTimeout) && ok;
+                tc_fence_after();
+                const uint32_t acc = tmem + b * (cols / 2) + (static_cast<uint32_t>(32 * quad) << 16);
+#pragma unroll
+                for (int g = 0; g < GH; ++g) {
+                    if (16 * (2 * g + half) >= a.rn) break;
+                    float w[16];
+                    tmem_ld16(acc + 16 * (2 * g + half), w);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) v[g][i] += w[i];
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&acc_empty[b]);
+            }
             // a wait that ran out ends all eight warps together: they share barriers
-            const bool ok = mbar_wait_bounded(&acc_full[b], static_cast<uint32_t>((seg >> 1) & 1), kLmTimeout);
             if (!named_bar_and(1, kLmEpiWarps * 32, ok)) break;
-            tc_fence_after();
-            const uint32_t acc = tmem + b * (cols / 2) + (static_cast<uint32_t>(32 * quad) << 16);
             float* mine = a.part + (static_cast<size_t>(blockIdx.x) + tile) * a.R * kLmTile + row;
-            for (int gi = half; gi < a.rn / 16; gi += 2) {
-                float v[16];
-                tmem_ld16(acc + 16 * gi, v);
+#pragma unroll
+            for (int g = 0; g < GH; ++g) {
+                const int gi = 2 * g + half;
+                if (16 * gi >= a.rn) break;
                 if (c0 == c1) {
-                    lm_write_v(a, tile, gi, row, scale, v);
+                    lm_write_v(a, tile, gi, row, scale, v[g]);
                 } else {
 #pragma unroll
                     for (int i = 0; i < 16; ++i)
-                        if (16 * gi + i < a.R) mine[(16 * gi + i) * kLmTile] = v[i];
+                        if (16 * gi + i < a.R) mine[(16 * gi + i) * kLmTile] = v[g][i];
                 }
             }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&acc_empty[b]);
             if (c0 != c1) {
                 __threadfence();
                 named_bar_sync(1, kLmEpiWarps * 32);
@@ -564,19 +707,24 @@ __global__ void __launch_bounds__(kLmThreads) lora_shrink_kernel(const __grid_co
                 named_bar_sync(1, kLmEpiWarps * 32);
                 if (s_last) {
                     for (int gi = half; gi < a.rn / 16; gi += 2) {
-                        float v[16];
+                        float t[16];
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) v[i] = 0.0f;
-                        for (int c = c0; c <= c1; ++c) {
-                            const float* p = a.part + (static_cast<size_t>(c) + tile) * a.R * kLmTile + row;
-                            float w[16];
+                        for (int i = 0; i < 16; ++i) t[i] = 0.0f;
+                        for (int c = c0; c <= c1; c += 4) {     // the loads of four partials at a time
+                            float w[4][16];
 #pragma unroll
-                            for (int i = 0; i < 16; ++i)
-                                w[i] = 16 * gi + i < a.R ? __ldcg(p + (16 * gi + i) * kLmTile) : 0.0f;
+                            for (int q = 0; q < 4; ++q) {
+                                const float* p = a.part + (static_cast<size_t>(c + q) + tile) * a.R * kLmTile + row;
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) v[i] += w[i];
+                                for (int i = 0; i < 16; ++i)
+                                    w[q][i] = c + q <= c1 && 16 * gi + i < a.R ? __ldcg(p + (16 * gi + i) * kLmTile) : 0.0f;
+                            }
+#pragma unroll
+                            for (int q = 0; q < 4; ++q)
+#pragma unroll
+                                for (int i = 0; i < 16; ++i) t[i] += w[q][i];
                         }
-                        lm_write_v(a, tile, gi, row, scale, v);
+                        lm_write_v(a, tile, gi, row, scale, t);
                     }
                 }
             }
@@ -585,16 +733,15 @@ __global__ void __launch_bounds__(kLmThreads) lora_shrink_kernel(const __grid_co
     }
     mbar_wait_bounded(&done, 0u, kLmTimeout);
     __syncthreads();
-    if (threadIdx.x == 0) lm_drain(full, S, s_issued);
+    if (threadIdx.x == 0) lm_drain(a_full, S, s_issued);
     tc_fence_after();
     __syncthreads();
     if (warp == 0) tmem_dealloc(tmem, cols);
 }
 
 template <typename O>
-__global__ void __launch_bounds__(kLmThreads) lora_expand_kernel(const __grid_constant__ CUtensorMap vmap,
+__global__ void __launch_bounds__(kLmThreads, 1) lora_expand_kernel(const __grid_constant__ CUtensorMap vmap,
                                                                  const __grid_constant__ CUtensorMap bmap,
-                                                                 const __grid_constant__ CUtensorMap basemap,
                                                                  const LmArgs a) {
     constexpr int kSubCols = 128 / sizeof(O);          // columns of a 128-byte row piece
     constexpr int kSubs = kLmCols / kSubCols;
@@ -607,7 +754,7 @@ __global__ void __launch_bounds__(kLmThreads) lora_expand_kernel(const __grid_co
     __shared__ __align__(8) uint64_t v_full[2], v_empty[2], b_full[kLmMaxStages], b_empty[kLmMaxStages],
         base_full[kLmMaxStages], base_empty[kLmMaxStages], acc_full[2], acc_empty[2], done;
     __shared__ uint32_t s_tmem;
-    __shared__ int s_issued[3];
+    __shared__ int s_issued[2];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     constexpr uint32_t kCols = 2 * kLmCols;
     if (threadIdx.x == 0) {
@@ -622,11 +769,11 @@ __global__ void __launch_bounds__(kLmThreads) lora_expand_kernel(const __grid_co
             mbar_init(&b_empty[i], 1);
         }
         for (int i = 0; i < a.base_stages; ++i) {
-            mbar_init(&base_full[i], 1);
+            mbar_init(&base_full[i], 128);
             mbar_init(&base_empty[i], kLmEpiWarps / 2);
         }
         mbar_init(&done, 1);
-        s_issued[0] = s_issued[1] = s_issued[2] = 0;
+        s_issued[0] = s_issued[1] = 0;
         fence_mbar_init();
     }
     if (warp == 0) {
@@ -637,7 +784,8 @@ __global__ void __launch_bounds__(kLmThreads) lora_expand_kernel(const __grid_co
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = s_tmem;
-    griddep_wait();
+    // The plan was complete before the shrink kernel started, base and B before
+    // that: they are fetched at once, only v waits for the shrink kernel.
     griddep_launch();
 
     const int C = (a.N + kLmCols - 1) / kLmCols;
@@ -645,63 +793,67 @@ __global__ void __launch_bounds__(kLmThreads) lora_expand_kernel(const __grid_co
     const int64_t u0 = U * blockIdx.x / G, u1 = U * (blockIdx.x + 1) / G;
 
     if (warp == 0) {
-        Ring rv, rb, rx;
-        int nv = 0, nb = 0, nx = 0;
-        bool ok = true;
-        int cur = -1;
-        LmTile t{};
-        int4 rows = make_int4(0, 0, 0, 0);
-        for (int64_t u = u0; u < u1; ++u) {
-            const int tile = static_cast<int>(u / C), n0 = static_cast<int>(u % C) * kLmCols;
-            if (tile != cur) {
-                cur = tile;
-                t = a.tiles[tile];
-                rows = lm_rows(a, t, lane);
-                ok = nv < a.v_bufs || mbar_wait_bounded(&v_empty[rv.slot], static_cast<uint32_t>(rv.phase ^ 1), kLmTimeout);
-                ok = __all_sync(0xffffffffu, ok);
+        if (lane == 0) {
+            Ring rv, rb;
+            int nv = 0, nb = 0, cur = -1, adapter = 0;
+            bool ok = true;
+            for (int64_t u = u0; ok && u < u1; ++u) {
+                const int tile = static_cast<int>(u / C), n0 = static_cast<int>(u % C) * kLmCols;
+                const bool first = tile != cur;
+                if (first) {
+                    cur = tile;
+                    adapter = a.tiles[tile].adapter;
+                }
+                for (int s = 0; s < a.ks; ++s) {
+                    ok = nb < a.b_stages || mbar_wait_bounded(&b_empty[rb.slot], static_cast<uint32_t>(rb.phase ^ 1), kLmTimeout);
+                    if (!ok) break;
+                    mbar_arrive_expect_tx(&b_full[rb.slot], kLmSlabBytes);
+                    tma_load_2d(smem_addr(sb + static_cast<size_t>(rb.slot) * kLmSlabBytes), &bmap, s * kLmSlab,
+                                adapter * a.N + n0, &b_full[rb.slot]);
+                    ++nb;
+                    rb.next(a.b_stages);
+                }
                 if (!ok) break;
-                if (lane == 0) {
+                if (first) {
+                    if (nv == 0) griddep_wait();
+                    ok = nv < a.v_bufs || mbar_wait_bounded(&v_empty[rv.slot], static_cast<uint32_t>(rv.phase ^ 1), kLmTimeout);
+                    if (!ok) break;
                     mbar_arrive_expect_tx(&v_full[rv.slot], static_cast<uint32_t>(v_slabs * kLmSlabBytes));
                     for (int i = 0; i < v_slabs; ++i)
                         tma_load_2d(smem_addr(sv + static_cast<size_t>(rv.slot * v_slabs + i) * kLmSlabBytes), &vmap, 0,
                                     (tile * v_slabs + i) * kLmTile, &v_full[rv.slot]);
+                    ++nv;
+                    rv.next(a.v_bufs);
                 }
-                __syncwarp();
-                ++nv;
-                rv.next(a.v_bufs);
             }
-            for (int s = 0; s < a.ks; ++s) {
-                ok = nb < a.b_stages || mbar_wait_bounded(&b_empty[rb.slot], static_cast<uint32_t>(rb.phase ^ 1), kLmTimeout);
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok) break;
-                if (lane == 0) {
-                    mbar_arrive_expect_tx(&b_full[rb.slot], kLmSlabBytes);
-                    tma_load_2d(smem_addr(sb + static_cast<size_t>(rb.slot) * kLmSlabBytes), &bmap, s * kLmSlab,
-                                t.adapter * a.N + n0, &b_full[rb.slot]);
-                }
-                __syncwarp();
-                ++nb;
-                rb.next(a.b_stages);
+            s_issued[0] = nv, s_issued[1] = nb;
+        }
+        __syncwarp();
+    } else if (warp >= kLmLoadWarp) {
+        RowLoader rows(threadIdx.x - kLmLoadWarp * 32);
+        Ring rx;
+        int nx = 0, cur = -1;
+        bool ok = true;
+        const size_t pitch = static_cast<size_t>(a.N) * sizeof(O);
+        for (int64_t u = u0; ok && u < u1; ++u) {
+            const int tile = static_cast<int>(u / C), n0 = static_cast<int>(u % C) * kLmCols;
+            if (tile != cur) {
+                cur = tile;
+                rows.tile(a, a.tiles[tile]);
             }
-            if (!ok) break;
-            const int quads = (t.count + 3) / 4;
             for (int s = 0; s < kSubs && n0 + s * kSubCols < a.N; ++s) {
                 ok = nx < a.base_stages ||
                      mbar_wait_bounded(&base_empty[rx.slot], static_cast<uint32_t>(rx.phase ^ 1), kLmTimeout);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
-                if (lane == 0) mbar_arrive_expect_tx(&base_full[rx.slot], static_cast<uint32_t>(quads * 512));
-                __syncwarp();
-                if (lane < quads)
-                    tma_gather4(smem_addr(sbase + static_cast<size_t>(rx.slot) * kLmSlabBytes) + 512 * lane, &basemap,
-                                n0 + s * kSubCols, rows, &base_full[rx.slot]);
+                rows.load(smem_addr(sbase) + rx.slot * kLmSlabBytes, a.base, pitch,
+                          static_cast<size_t>(n0 + s * kSubCols) * sizeof(O));
+                cp_async_arrive(&base_full[rx.slot]);
                 ++nx;
                 rx.next(a.base_stages);
             }
-            if (!ok) break;
         }
-        if (lane == 0) s_issued[0] = nv, s_issued[1] = nb, s_issued[2] = nx;
-        __syncwarp();
+        cp_async_wait_all();
     } else if (warp == 1) {
         if (lane == 0) {
             Ring rv, rb;
@@ -751,11 +903,15 @@ __global__ void __launch_bounds__(kLmThreads) lora_expand_kernel(const __grid_co
     } else if (warp < 4) {
         // rows of tokens without an adapter
         if (a.out != a.base) {
+            // one row at a time to a warp: such tokens come in long runs
             const size_t row_bytes = static_cast<size_t>(a.N) * sizeof(O);
-            for (int t0 = (blockIdx.x * 2 + warp - 2) * 32; t0 < a.T; t0 += gridDim.x * 64) {
-                uint32_t none = __ballot_sync(0xffffffffu, t0 + lane < a.T && a.row_idx[min(t0 + lane, a.T - 1)] < 0);
+            const int64_t step = gridDim.x * 2;
+            for (int64_t t0 = blockIdx.x * 2 + warp - 2; t0 < a.T; t0 += 32 * step) {
+                const int64_t t = t0 + lane * step;
+                const int id = t < a.T ? a.ids[t] : 0;
+                uint32_t none = __ballot_sync(0xffffffffu, id < 0 || id >= a.L);
                 for (; none != 0; none &= none - 1) {
-                    const size_t at = static_cast<size_t>(t0 + __ffs(none) - 1) * row_bytes;
+                    const size_t at = static_cast<size_t>(t0 + (__ffs(none) - 1) * step) * row_bytes;
                     const uint8_t* src = static_cast<const uint8_t*>(a.base) + at;
                     uint8_t* dst = static_cast<uint8_t*>(a.out) + at;
 #pragma unroll 8
@@ -829,7 +985,6 @@ __global__ void __launch_bounds__(kLmThreads) lora_expand_kernel(const __grid_co
                     if (r < count && col < a.N)
                         st_v4(static_cast<O*>(a.out) + static_cast<size_t>(token[it]) * a.N + col, w);
                 }
-                fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&base_empty[rx.slot]);
             }
@@ -844,8 +999,8 @@ __global__ void __launch_bounds__(kLmThreads) lora_expand_kernel(const __grid_co
     if (threadIdx.x == 0) {
         lm_drain(v_full, a.v_bufs, s_issued[0]);
         lm_drain(b_full, a.b_stages, s_issued[1]);
-        lm_drain(base_full, a.base_stages, s_issued[2]);
     }
+    griddep_wait();   // every CTA, also one without work: this kernel ends behind the shrink kernel
     tc_fence_after();
     __syncthreads();
     if (warp == 0) tmem_dealloc(tmem, kCols);
@@ -855,7 +1010,9 @@ int lm_most_tiles(int T, int L) { return (T + kLmTile - 1) / kLmTile + (L < T ? 
 int lm_parts(bool bf16) { return bf16 ? 2 : 3; }
 size_t lm_pad(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
 
-// The workspace of the many-token path, in order; `base` NULL only sizes it.
+bool lm_one_plan(int T, int L) { return T <= kLmPlanTokens && L <= kLmPlanAdapters; }
+
+// The workspace of the many-token path, in order.
 struct LmLayout {
     size_t offsets, row_idx, row_token, dispatch, tiles, ntiles, arrived, part, v, bytes;
 };
@@ -868,10 +1025,11 @@ LmLayout lm_layout(int T, int H, int R, int L) {
         at += lm_pad(n);
         return p;
     };
-    l.offsets = take((static_cast<size_t>(L) + 1) * 4);
-    l.row_idx = take(static_cast<size_t>(T) * 4);
     l.row_token = take(static_cast<size_t>(T) * 4);
-    l.dispatch = take(dispatch_workspace_bytes(T, L));
+    const bool big = !lm_one_plan(T, L);
+    l.offsets = take(big ? (static_cast<size_t>(L) + 1) * 4 : 0);
+    l.row_idx = take(big ? static_cast<size_t>(T) * 4 : 0);
+    l.dispatch = take(big ? dispatch_workspace_bytes(T, L) : 0);
     l.tiles = take(nt * sizeof(LmTile));
     l.ntiles = take(4);
     l.arrived = take(nt * 4);
@@ -902,7 +1060,7 @@ cudaError_t launch_lora_many(const LoraLaunch& l, cudaStream_t s) {
     int32_t* offsets = reinterpret_cast<int32_t*>(w + at.offsets);
     int32_t* row_idx = reinterpret_cast<int32_t*>(w + at.row_idx);
     int32_t* row_token = reinterpret_cast<int32_t*>(w + at.row_token);
-    a.offsets = offsets, a.row_idx = row_idx, a.row_token = row_token;
+    a.ids = l.ids, a.x = l.x, a.offsets = offsets, a.row_token = row_token;
     a.tiles = reinterpret_cast<LmTile*>(w + at.tiles);
     a.ntiles = reinterpret_cast<int32_t*>(w + at.ntiles);
     a.arrived = reinterpret_cast<int32_t*>(w + at.arrived);
@@ -913,42 +1071,51 @@ cudaError_t launch_lora_many(const LoraLaunch& l, cudaStream_t s) {
     a.rn = (l.R + 15) / 16 * 16;
     a.ks = (l.R + kLmSlab - 1) / kLmSlab;
     a.parts = lm_parts(l.bf16);
-    a.stages = kLmBytes / (kLmSlabBytes + a.rn * 128);
+    a.stages = kLmBytes / (kLmStep * (kLmSlabBytes + a.rn * 128));
     if (a.stages > kLmMaxStages) a.stages = kLmMaxStages;
     // the expand kernel's 13 slabs of 16 KB: v (twice while it is one slab wide), B, and the rest base
     a.v_bufs = a.ks == 1 ? 2 : 1;
     a.b_stages = a.ks == 1 ? 2 : 3;
     a.base_stages = kLmBytes / kLmSlabBytes - a.v_bufs * a.parts * a.ks - a.b_stages;
-    CUtensorMap xmap, amap, vmap, bmap, basemap;
+    CUtensorMap amap, vmap, bmap;
     constexpr auto kBf16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
     constexpr auto kSw = CU_TENSOR_MAP_SWIZZLE_128B;
     const uint64_t v_rows = static_cast<uint64_t>(lm_most_tiles(l.T, l.L)) * a.parts * a.ks * kLmTile;
-    if (!encode_2d_map(&xmap, kBf16, 2, l.x, l.T, l.H, static_cast<uint64_t>(l.H) * 2, 1, kLmSlab, kSw) ||
-        !encode_2d_map(&amap, kBf16, 2, l.a, static_cast<uint64_t>(l.L) * l.R, l.H, static_cast<uint64_t>(l.H) * 2,
+    if (!encode_2d_map(&amap, kBf16, 2, l.a, static_cast<uint64_t>(l.L) * l.R, l.H, static_cast<uint64_t>(l.H) * 2,
                        static_cast<uint32_t>(a.rn), kLmSlab, kSw) ||
         !encode_2d_map(&vmap, kBf16, 2, a.v, v_rows, kLmSlab, kLmSlab * 2, kLmTile, kLmSlab, kSw) ||
         !encode_2d_map(&bmap, kBf16, 2, l.b, static_cast<uint64_t>(l.L) * l.N, l.R, static_cast<uint64_t>(l.R) * 2,
-                       kLmCols, kLmSlab, kSw) ||
-        !encode_2d_map(&basemap, l.bf16 ? kBf16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, l.bf16 ? 2 : 4, l.base, l.T, l.N,
-                       static_cast<uint64_t>(l.N) * (l.bf16 ? 2 : 4), 1, l.bf16 ? 64 : 32, kSw))
+                       kLmCols, kLmSlab, kSw))
         return cudaErrorInvalidValue;
-    cudaError_t e = launch_dispatch(l.ids, l.T, 1, 0, l.L, offsets, row_idx, row_token, w + at.dispatch, s);
-    if (e != cudaSuccess) return e;
+    cudaError_t e;
     void* targs[] = {&a};
-    e = lm_launch(reinterpret_cast<const void*>(lora_tiles_kernel), 1, 1024, 0, targs, s);
+    if (lm_one_plan(l.T, l.L)) {
+        const void* plan = reinterpret_cast<const void*>(lora_plan_kernel);
+        const size_t psmem = static_cast<size_t>((l.T + 7) / 8 * 8 + 32 * l.L) * 2;
+        e = cudaFuncSetAttribute(plan, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 (kLmPlanTokens + 32 * kLmPlanAdapters) * 2);
+        if (e == cudaSuccess) e = lm_launch(plan, 1, 1024, psmem, targs, s);
+    } else {
+        e = launch_dispatch(l.ids, l.T, 1, 0, l.L, offsets, row_idx, row_token, w + at.dispatch, s);
+        if (e == cudaSuccess) e = lm_launch(reinterpret_cast<const void*>(lora_tiles_kernel), 1, 1024, 0, targs, s);
+    }
     if (e != cudaSuccess) return e;
     const int smem = kLmBytes + 1024;
-    const void* shrink = reinterpret_cast<const void*>(lora_shrink_kernel);
+    const void* const shrinks[] = {reinterpret_cast<const void*>(lora_shrink_kernel<1>),
+                                   reinterpret_cast<const void*>(lora_shrink_kernel<2>),
+                                   reinterpret_cast<const void*>(lora_shrink_kernel<3>),
+                                   reinterpret_cast<const void*>(lora_shrink_kernel<4>)};
+    const void* shrink = shrinks[(a.rn + 31) / 32 - 1];
     const void* expand = l.bf16 ? reinterpret_cast<const void*>(lora_expand_kernel<uint16_t>)
                                 : reinterpret_cast<const void*>(lora_expand_kernel<float>);
     for (const void* k : {shrink, expand}) {
         e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
     }
-    void* sargs[] = {&xmap, &amap, &a};
+    void* sargs[] = {&amap, &a};
     e = lm_launch(shrink, device_info().sm_count, kLmThreads, smem, sargs, s);
     if (e != cudaSuccess) return e;
-    void* eargs[] = {&vmap, &bmap, &basemap, &a};
+    void* eargs[] = {&vmap, &bmap, &a};
     return lm_launch(expand, device_info().sm_count, kLmThreads, smem, eargs, s);
 }
 
