@@ -521,7 +521,7 @@ def moe_balance_loss(logits: torch.Tensor, topk_ids: torch.Tensor, token_mask: t
     ``seq_offsets`` (int32 [Q + 1] on the device, ascending) cuts the tokens
     into the sequences the loss is averaged over; without it the batch is one.
     ``workspace`` is a uint8 CUDA tensor of at least ``balance_workspace_size``
-    bytes; when omitted, one is allocated here."""
+    bytes (0 for small batches); when omitted, one is allocated here."""
     fn = "moe_balance_loss"
     T, E, k, Q = _router_batch(fn, logits, topk_ids, token_mask, seq_offsets)
     dev = logits.device
@@ -534,16 +534,20 @@ def moe_balance_loss(logits: torch.Tensor, topk_ids: torch.Tensor, token_mask: t
     if seq_tokens is None:
         seq_tokens = torch.empty(Q, dtype=torch.int32, device=dev)
     if workspace is None:
-        workspace = torch.empty(balance_workspace_size(T, E, Q), dtype=torch.uint8, device=dev)
-    for t, dt, name in ((loss, torch.float32, "loss"), (counts, torch.int32, "counts"),
-                        (prob_sums, torch.float32, "prob_sums"), (seq_tokens, torch.int32, "seq_tokens"),
-                        (workspace, torch.uint8, "workspace")):
-        _want(t, dt, name)
+        need = load().moe_balance_workspace_size(T, E, Q)
+        if need > 0:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    else:
+        _want(workspace, torch.uint8, "workspace")
+    _want(loss, torch.float32, "loss")
+    _want(counts, torch.int32, "counts")
+    _want(prob_sums, torch.float32, "prob_sums")
+    _want(seq_tokens, torch.int32, "seq_tokens")
     if loss.numel() != 1 or counts.shape != (Q, E) or prob_sums.shape != (Q, E) or seq_tokens.numel() != Q:
         raise ValueError(f"{fn}: shape mismatch")
     _enqueue(fn, (logits, topk_ids, token_mask, loss, counts, prob_sums, seq_tokens, workspace, seq_offsets), stream,
              _at(logits), _at(topk_ids), _at(token_mask), T, E, k, _at(seq_offsets), Q, coeff, _at(loss), _at(counts),
-             _at(prob_sums), _at(seq_tokens), _at(workspace), workspace.numel())
+             _at(prob_sums), _at(seq_tokens), _at(workspace), 0 if workspace is None else workspace.numel())
     return loss, counts, prob_sums, seq_tokens
 
 

@@ -409,10 +409,12 @@ int moe_balance_loss(const float* logits, const int32_t* topk_ids, const uint8_t
         !aligned16(counts) || !aligned16(prob_sums) || !aligned16(seq_tokens))
         return fail(MB_ERR_INVALID_ARG, "%s: pointers must be 16-byte aligned", fn);
     const size_t need = balance_workspace_bytes(T, E, Q);
-    if (!workspace || workspace_bytes < need)
-        return fail(MB_ERR_INVALID_ARG, "%s: needs a workspace of %zu bytes (got %zu)", fn, need,
-                    workspace ? workspace_bytes : static_cast<size_t>(0));
-    if (!aligned16(workspace)) return fail(MB_ERR_INVALID_ARG, "%s: workspace must be 16-byte aligned", fn);
+    if (need > 0) {
+        if (!workspace || workspace_bytes < need)
+            return fail(MB_ERR_INVALID_ARG, "%s: needs a workspace of %zu bytes (got %zu)", fn, need,
+                        workspace ? workspace_bytes : static_cast<size_t>(0));
+        if (!aligned16(workspace)) return fail(MB_ERR_INVALID_ARG, "%s: workspace must be 16-byte aligned", fn);
+    }
     const BalanceLaunch b{logits, topk_ids, token_mask, seq_offsets, T, E, k, Q, coeff, loss, counts, prob_sums,
                           seq_tokens, workspace};
     return cuda_status(launch_balance_loss(b, static_cast<cudaStream_t>(stream)), fn);

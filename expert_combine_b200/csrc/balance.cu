@@ -13,10 +13,13 @@
 //
 // Both passes read every logit once, so DRAM bounds them (the backward pass
 // also writes as much as it reads); they need 2 special-function results (2^x
-// and a reciprocal) per logit.  A row of E logits stays in the registers of a
-// team of warps, at most 16 a lane: one warp up to E = 512, where the row's
-// sums are butterflies, then ceil(E / 512) warps that join their sums through
-// shared memory at one named barrier a row.
+// and a reciprocal) per logit.  A row of E logits belongs to a team of warps, at
+// most 16 logits a lane: one warp up to E = 512, where the row's sums are
+// butterflies, then ceil(E / 512) warps that join their sums through shared
+// memory at one named barrier a row.  Each warp streams its part of the team's
+// rows through a ring of its own in shared memory, filled by bulk copies that
+// its lane 0 starts up to 8 rows ahead, so loads need neither registers nor
+// warps in waiting (rows of E % 4 != 0 are read one ahead into registers).
 //
 // 1 - s is never formed by subtraction: with u = exp(-|x|), r = 1 / (1 + u),
 // s is r or u r by the sign of x and s (1 - s) = u r^2.  A row whose sigmoids
@@ -28,7 +31,9 @@
 // range is cut at the sequence borders, each piece leaves its sums in a slot
 // of its own (CTA b, sequence q: slot b + q, unique because both only grow
 // along the tokens), and a second kernel adds the slots of a sequence in a
-// fixed order.  Results do not depend on timing.
+// fixed order.  A small batch runs as one cluster of 8 CTAs whose slots are
+// their shared memory: one launch, no workspace.  Results do not depend on
+// timing.
 #include "internal.h"
 #include "common.cuh"
 
@@ -38,31 +43,48 @@ namespace {
 
 constexpr int kBalLane = 16;                 // most logits per lane
 constexpr int kBalMaxTeam = kMaxExperts / (32 * kBalLane);
-constexpr int kBalWarps = 8;                 // warps of a CTA (a multiple of the team below it)
-constexpr int kBalRowsPerTeam = 64;          // most rows a team adds up in one FP32 register
-constexpr int kBalTargetCtas = 148 * 3;
+constexpr int kBalWarps = 16;                // most warps of a CTA (one CTA per SM)
+constexpr int kBalRowsPerTeam = 128;         // most rows a team adds up in one FP32 register
+constexpr int kBalTargetCtas = 148;
+constexpr int kBalRing = 8;                  // most row slots of a warp
+constexpr int kBalRingBytes = 128 * 1024;    // of a CTA
 constexpr float kBalTinySum = 1e-20f;
+constexpr unsigned int kBalTimeout = 64u;    // bit 6 of the device status word
 constexpr int kFinExperts = 32, kFinLanes = 16;   // second kernel: experts x slot lanes per CTA
+constexpr int kBalCluster = 8;               // small batches: CTAs of the one cluster
+constexpr int kBalClusterLogits = 256 * 1024;     // T * E up to here (2 MB of logits through 8 SMs)
+constexpr int kBalClusterSums = 4096;             // Q * E up to here (32 KB of shared memory)
 
 struct BalPlan {
     int W;        // warps per team
     int teams;    // teams per CTA
     int nv;       // groups of 4 logits per lane
-    int rows;     // rows per team
     int tokens;   // tokens per CTA
     int ctas;
+    int ring;     // row slots per warp
+    bool cluster; // forward pass in one cluster
 };
 
-BalPlan bal_plan(int T, int E) {
+BalPlan bal_plan(int T, int E, int Q) {
     BalPlan p;
     p.W = (E + 32 * kBalLane - 1) / (32 * kBalLane);
     p.teams = kBalWarps / p.W;
     p.nv = (E + 128 * p.W - 1) / (128 * p.W);
-    int64_t rows = (static_cast<int64_t>(T) + static_cast<int64_t>(kBalTargetCtas) * p.teams - 1) /
-                   (static_cast<int64_t>(kBalTargetCtas) * p.teams);
-    p.rows = static_cast<int>(rows < 1 ? 1 : rows > kBalRowsPerTeam ? kBalRowsPerTeam : rows);
-    p.tokens = p.rows * p.teams;
+    p.cluster = static_cast<int64_t>(T) * E <= kBalClusterLogits && static_cast<int64_t>(Q) * E <= kBalClusterSums;
+    const int64_t ctas = p.cluster ? kBalCluster : kBalTargetCtas;
+    // as many rows a team as fill the card's teams, in several waves where that were more than kBalRowsPerTeam
+    const int64_t per = ctas * p.teams;
+    const int64_t waves = T == 0 ? 1 : (T + per * kBalRowsPerTeam - 1) / (per * kBalRowsPerTeam);
+    int64_t rows = (T + per * waves - 1) / (per * waves);
+    if (rows < 1) rows = 1;
+    p.tokens = static_cast<int>(rows) * p.teams;
     p.ctas = T == 0 ? 1 : static_cast<int>((static_cast<int64_t>(T) + p.tokens - 1) / p.tokens);
+    p.ring = 0;
+    if (E % 4 == 0) {
+        p.ring = (p.W == 1 ? kBalRingBytes : kBalRingBytes * 3 / 4) / (p.W * p.teams * p.nv * 512);
+        if (p.ring > kBalRing) p.ring = kBalRing;
+        if (p.ring > rows) p.ring = static_cast<int>(rows);
+    }
     return p;
 }
 
@@ -72,7 +94,7 @@ struct BalArgs {
     const uint8_t* mask;        // [T]
     const int32_t* offsets;     // [Q + 1] or NULL (one sequence)
     int T, E, k, Q;
-    int W, teams, tokens;
+    int W, teams, tokens, ring;
     float coeff;
     // forward
     float* slot_p;              // [ctas + Q][E]
@@ -101,6 +123,12 @@ __device__ __forceinline__ float rcp_approx(float t) {
     float r;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(t));
     return r;
+}
+// Store to `local`'s place in the shared memory of cluster rank `rank`.
+__device__ __forceinline__ void st_cluster(float* local, uint32_t rank, float v) {
+    uint32_t remote;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(smem_addr(local)), "r"(rank));
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(remote), "f"(v) : "memory");
 }
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -149,6 +177,12 @@ struct Team {
     }
     __device__ __forceinline__ float sum(float v) { return join<false>(make_float2(warp_tree_sum(v), 0.0f)).x; }
     __device__ __forceinline__ float max(float v) { return join<true>(make_float2(warp_max(v), 0.0f)).x; }
+    __device__ __forceinline__ void sync() {
+        if (W == 1)
+            __syncwarp();
+        else
+            named_bar_sync(bar, W * 32);
+    }
     template <bool MAX>
     __device__ __forceinline__ float2 join(float2 v) {
         if (W == 1) {
@@ -160,9 +194,12 @@ struct Team {
         if (lane == 0) buf[wt] = v;
         named_bar_sync(bar, W * 32);
         float2 a = buf[0];
-        for (int w = 1; w < W; ++w) {
-            a.x = MAX ? fmaxf(a.x, buf[w].x) : a.x + buf[w].x;
-            a.y += buf[w].y;
+#pragma unroll
+        for (int w = 1; w < kBalMaxTeam; ++w) {
+            if (w >= W) break;
+            const float2 o = buf[w];
+            a.x = MAX ? fmaxf(a.x, o.x) : a.x + o.x;
+            a.y += o.y;
         }
         return a;
     }
@@ -187,110 +224,289 @@ __device__ __forceinline__ int first_sequence(const BalArgs& a, int t) {
     return lo;
 }
 
+// This warp's part of its team's rows (tokens first, first + teams, ...), in
+// order, as pairs of logits.
 template <int NV, bool VEC>
-__global__ void __launch_bounds__(kBalWarps * 32) balance_kernel(const BalArgs a) {
+struct RowFeed {
+    const float* next;       // VEC: the warp's part of the next row to copy; else of the next row to read
+    size_t pitch;            // floats from row to row
+    int left;                // rows not yet copied (VEC) or read
+    int flying;              // rows copied or being copied, not yet taken
+    int slot, phase, ring, bytes, lane, wt, E;
+    float* slots;
+    uint64_t* full;
+    bool dead;
+    float ahead[VEC ? 1 : 4 * NV];
+
+    __device__ __forceinline__ void start(const BalArgs& a, const Team& tm, int warp, int first, int end, uint8_t* smem,
+                                          uint64_t* bars) {
+        lane = tm.lane, wt = tm.wt, E = a.E, ring = a.ring, slot = 0, phase = 0, flying = 0, dead = false;
+        left = first < end ? (end - first + a.teams - 1) / a.teams : 0;
+        pitch = static_cast<size_t>(a.teams) * a.E;
+        next = a.logits + static_cast<size_t>(first) * a.E;
+        if constexpr (VEC) {
+            next += wt * NV * 128;
+            slots = reinterpret_cast<float*>(smem) + static_cast<size_t>(warp) * ring * NV * 128;
+            full = bars + warp * kBalRing;
+            const int mine = E - wt * NV * 128;
+            bytes = 4 * (mine < 0 ? 0 : mine < NV * 128 ? mine : NV * 128);
+            if (bytes < NV * 512) {     // behind the row's end the copies write nothing: -inf stays there
+                for (int i = lane; i < ring * NV * 128; i += 32) slots[i] = -INFINITY;
+                fence_proxy_async_smem();
+                __syncwarp();
+            }
+            if (bytes == 0) left = 0;
+            for (int i = 0; i < ring && left > 0; ++i) {
+                if (lane == 0) copy(i);
+                advance();
+            }
+        } else {
+            if (left > 0) bal_load<NV, VEC>(next, E, wt, lane, ahead);
+        }
+    }
+    __device__ __forceinline__ void copy(int s) {
+        mbar_arrive_expect_tx(&full[s], static_cast<uint32_t>(bytes));
+        bulk_g2s(slots + s * NV * 128, next, static_cast<uint32_t>(bytes), &full[s]);
+    }
+    __device__ __forceinline__ void advance() {
+        next += pitch;
+        --left;
+        ++flying;
+    }
+    // The next row.
+    __device__ __forceinline__ void take(float2 (&x)[2 * NV]) {
+        if constexpr (VEC) {
+            // after a wait that ran out the values are not the row's, but the team keeps its barriers
+            if (flying > 0 && !dead) dead = !mbar_wait_bounded(&full[slot], static_cast<uint32_t>(phase), kBalTimeout);
+            const float* p = slots + slot * NV * 128 + 4 * lane;
+#pragma unroll
+            for (int v = 0; v < NV; ++v) {
+                const float4 f = *reinterpret_cast<const float4*>(p + 128 * v);
+                x[2 * v] = make_float2(f.x, f.y), x[2 * v + 1] = make_float2(f.z, f.w);
+            }
+            if (flying > 0) {
+                --flying;
+                __syncwarp();      // every lane has its values: the slot is free
+                if (left > 0 && !dead) {
+                    if (lane == 0) {
+                        fence_proxy_async_smem();
+                        copy(slot);
+                    }
+                    advance();
+                }
+                if (++slot == ring) slot = 0, phase ^= 1;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 2 * NV; ++i) x[i] = make_float2(ahead[2 * i], ahead[2 * i + 1]);
+            next += pitch;
+            if (--left > 0) bal_load<NV, VEC>(next, E, wt, lane, ahead);
+        }
+    }
+    // Copies that were started and not used land before the CTA ends.
+    __device__ __forceinline__ void drain() {
+        if constexpr (VEC)
+            if (lane == 0)
+                for (; flying > 0; --flying) {
+                    mbar_wait_bounded(&full[slot], static_cast<uint32_t>(phase), kBalTimeout);
+                    if (++slot == ring) slot = 0, phase ^= 1;
+                }
+    }
+};
+
+// Which of a team's rows are valid tokens, 32 rows at a time (one byte a lane),
+// the next 32 already on their way.
+struct RowMask {
+    const uint8_t* p;        // this lane's next byte
+    int64_t t, end, step;
+    uint32_t bits, byte;
+    int at;
+    __device__ __forceinline__ void start(const BalArgs& a, int lane, int first, int last) {
+        step = 32 * static_cast<int64_t>(a.teams);
+        t = first + static_cast<int64_t>(lane) * a.teams;
+        end = last;
+        p = a.mask + t;
+        at = 32;
+        fetch();
+    }
+    __device__ __forceinline__ void fetch() {
+        byte = t < end ? *p : 0;
+        t += step;
+        p += step;
+    }
+    __device__ __forceinline__ bool next() {
+        if (at == 32) {
+            bits = __ballot_sync(0xffffffffu, byte != 0);
+            at = 0;
+            fetch();
+        }
+        return bits >> at++ & 1u;
+    }
+};
+
+// Shared memory of the CTA: the warps' rings, then what the kernel adds.
+template <int NV>
+__host__ __device__ __forceinline__ size_t bal_ring_bytes(int warps, int ring) {
+    return static_cast<size_t>(warps) * ring * NV * 512;
+}
+
+// CL: one cluster of kBalCluster CTAs does all; the slots are shared memory.
+template <int NV, bool VEC, bool CL>
+__global__ void __launch_bounds__(kBalWarps * 32, 1) balance_kernel(const BalArgs a) {
     constexpr int NE = 4 * NV;
-    extern __shared__ __align__(16) uint8_t bal_smem[];
-    float* sums = reinterpret_cast<float*>(bal_smem);                    // [teams][E]
+    extern __shared__ __align__(128) uint8_t bal_smem[];
+    float* sums = reinterpret_cast<float*>(bal_smem + bal_ring_bytes<NV>(a.W * a.teams, a.ring));   // [teams][E]
     int32_t* hist = reinterpret_cast<int32_t*>(sums + a.teams * a.E);    // [E]
+    float* own_p = reinterpret_cast<float*>(hist + a.E);                 // CL: [Q][E]
+    int32_t* own_c = reinterpret_cast<int32_t*>(own_p + a.Q * a.E);      // CL: [Q][E]
+    int32_t* own_n = own_c + a.Q * a.E;                                  // CL: [Q]
+    float* own_l = reinterpret_cast<float*>(own_n + a.Q);                // CL: [Q] losses (rank 0)
     __shared__ float2 red[kBalWarps][2 * kBalMaxTeam];
+    __shared__ __align__(8) uint64_t bars[kBalWarps * kBalRing];
     __shared__ int s_n;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int team = warp / a.W;
     Team tm{red[team], a.W, 1 + team, warp % a.W, lane, 0};
-    const int64_t t0 = static_cast<int64_t>(blockIdx.x) * a.tokens;
-    const int t1 = static_cast<int>(min(t0 + a.tokens, static_cast<int64_t>(a.T)));
-
+    for (int i = threadIdx.x; i < kBalWarps * kBalRing; i += blockDim.x) mbar_init(&bars[i], 1);
     for (int e = threadIdx.x; e < a.E; e += blockDim.x) hist[e] = 0;
+    if (CL)
+        for (int i = threadIdx.x; i < a.Q * (2 * a.E + 2); i += blockDim.x) own_c[i - a.Q * a.E] = 0;
     if (threadIdx.x == 0) s_n = 0;
+    fence_mbar_init();
     griddep_wait();
     griddep_launch();
-    if (blockIdx.x == 0 && threadIdx.x == 0) *a.ticket = 0u;
+    if (!CL && blockIdx.x == 0 && threadIdx.x == 0) *a.ticket = 0u;
     __syncthreads();
 
-    for (int q = first_sequence(a, static_cast<int>(t0)); q < a.Q; ++q) {
-        const int lo = clamp_offset(a, q);
-        if (lo >= t1) break;
-        const int s = max(static_cast<int>(t0), lo), e_ = min(t1, clamp_offset(a, q + 1));
-        if (s >= e_) continue;
+    // this CTA's tokens that belong to a sequence
+    const int64_t c0 = static_cast<int64_t>(blockIdx.x) * a.tokens;
+    const int t0 = max(static_cast<int>(min(c0, static_cast<int64_t>(a.T))), clamp_offset(a, 0));
+    const int t1 = min(static_cast<int>(min(c0 + a.tokens, static_cast<int64_t>(a.T))), clamp_offset(a, a.Q));
+    RowFeed<NV, VEC> feed;
+    feed.start(a, tm, warp, t0 + team, t1, bal_smem, bars);
+    RowMask mask;
+    mask.start(a, lane, t0 + team, t1);
+    int t = t0 + team;
+    const bool counts = tm.wt == 0 && lane < a.k;
+    const int32_t* pick = a.ids + static_cast<size_t>(t < t1 ? t : 0) * a.k + lane;
+    const size_t pick_step = static_cast<size_t>(a.teams) * a.k;
+    int id = counts && t < t1 ? *pick : -1, id1 = counts && t + a.teams < t1 ? pick[pick_step] : -1;   // two rows ahead
+    pick += 2 * pick_step;
 
-        float acc[NE];
+    for (int q = first_sequence(a, t0); t0 < t1 && q < a.Q; ++q) {
+        const int lo = clamp_offset(a, q), hi = min(t1, clamp_offset(a, q + 1));
+        if (lo >= t1) break;
+        if (max(t0, lo) >= hi) continue;
+
+        float2 acc[NE / 2];
 #pragma unroll
-        for (int i = 0; i < NE; ++i) acc[i] = 0.0f;
+        for (int i = 0; i < NE / 2; ++i) acc[i] = make_float2(0.0f, 0.0f);
         int n = 0;
-        float x[NE];
-        bool valid = false;
-        int id = -1;
-        auto fetch = [&](int t, float (&xx)[NE], bool& v, int& d) {
-            v = false;
-            if (t < e_) {
-                bal_load<NV, VEC>(a.logits + static_cast<size_t>(t) * a.E, a.E, tm.wt, lane, xx);
-                v = a.mask[t] != 0;
-                if (tm.wt == 0) d = lane < a.k ? a.ids[static_cast<size_t>(t) * a.k + lane] : -1;
-            }
-        };
-        fetch(s + team, x, valid, id);
-        for (int t = s + team; t < e_; t += a.teams) {
-            float xn[NE];
-            bool nvalid;
-            int nid = -1;
-            fetch(t + a.teams, xn, nvalid, nid);
-            if (valid) {
-                float loc = 0.0f;
-                float sg[NE];
+        for (; t < hi; t += a.teams) {
+            float2 x[NE / 2];
+            feed.take(x);
+            const bool valid = mask.next();
+            const int id2 = counts && t + 2 * a.teams < t1 ? *pick : -1;
+            pick += pick_step;
+            if (valid && t >= lo) {
+                float2 loc = make_float2(0.0f, 0.0f);
 #pragma unroll
-                for (int i = 0; i < NE; ++i) {
-                    sg[i] = rcp_approx(1.0f + ex2_approx(x[i] * -kLog2e));
-                    loc += sg[i];
+                for (int i = 0; i < NE / 2; ++i) {
+                    const float2 e = mul2(x[i], make_float2(-kLog2e, -kLog2e));
+                    const float2 d = add2(make_float2(ex2_approx(e.x), ex2_approx(e.y)), make_float2(1.0f, 1.0f));
+                    x[i] = make_float2(rcp_approx(d.x), rcp_approx(d.y));
+                    loc = add2(loc, x[i]);
                 }
-                float S = tm.sum(loc);
-                if (S < kBalTinySum) {
-                    float m = -INFINITY;
+                float S = tm.sum(loc.x + loc.y);
+                float inv = rcp_approx(S);
+                if (S < kBalTinySum) {      // once more, relative to the row's largest
+                    float y[NE], m = -INFINITY, sum = 0.0f;
+                    bal_load<NV, VEC>(a.logits + static_cast<size_t>(t) * a.E, a.E, tm.wt, lane, y);
 #pragma unroll
-                    for (int i = 0; i < NE; ++i) m = fmaxf(m, x[i]);
+                    for (int i = 0; i < NE; ++i) m = fmaxf(m, y[i]);
                     m = tm.max(m);
-                    loc = 0.0f;
 #pragma unroll
                     for (int i = 0; i < NE; ++i) {
-                        sg[i] = m == -INFINITY ? 0.0f : ex2_approx((x[i] - m) * kLog2e);
-                        loc += sg[i];
+                        y[i] = m == -INFINITY ? 0.0f : ex2_approx((y[i] - m) * kLog2e);
+                        sum += y[i];
                     }
-                    S = tm.sum(loc);
-                }
-                const float inv = S == 0.0f ? 0.0f : __frcp_rn(S);
+                    S = tm.sum(sum);
+                    inv = S == 0.0f ? 0.0f : rcp_approx(S);
 #pragma unroll
-                for (int i = 0; i < NE; ++i) acc[i] = fmaf(sg[i], inv, acc[i]);
-                if (tm.wt == 0) {
-                    if (id >= 0 && id < a.E) atomicAdd(&hist[id], 1);
-                    ++n;
+                    for (int i = 0; i < NE / 2; ++i) x[i] = make_float2(y[2 * i], y[2 * i + 1]);
                 }
+#pragma unroll
+                for (int i = 0; i < NE / 2; ++i) acc[i] = fma2(x[i], make_float2(inv, inv), acc[i]);
+                if (id >= 0 && id < a.E) atomicAdd(&hist[id], 1);
+                ++n;
             }
-#pragma unroll
-            for (int i = 0; i < NE; ++i) x[i] = xn[i];
-            valid = nvalid;
-            id = nid;
+            id = id1, id1 = id2;
         }
 #pragma unroll
-        for (int i = 0; i < NE; ++i) {
-            const int e = bal_expert<NV, VEC>(tm.wt, lane, i);
-            if (e < a.E) sums[team * a.E + e] = acc[i];
+        for (int i = 0; i < NE / 2; ++i) {
+            const int e0 = bal_expert<NV, VEC>(tm.wt, lane, 2 * i), e1 = bal_expert<NV, VEC>(tm.wt, lane, 2 * i + 1);
+            if (e0 < a.E) sums[team * a.E + e0] = acc[i].x;
+            if (e1 < a.E) sums[team * a.E + e1] = acc[i].y;
         }
         if (tm.wt == 0 && lane == 0 && n) atomicAdd(&s_n, n);
         __syncthreads();
-        const size_t slot = static_cast<size_t>(blockIdx.x) + q;
+        const size_t slot = CL ? static_cast<size_t>(q) : static_cast<size_t>(blockIdx.x) + q;
+        float* dst_p = (CL ? own_p : a.slot_p) + slot * a.E;
+        int32_t* dst_c = (CL ? own_c : a.slot_c) + slot * a.E;
         for (int e = threadIdx.x; e < a.E; e += blockDim.x) {
             float p = sums[e];
             for (int m = 1; m < a.teams; ++m) p += sums[m * a.E + e];
-            a.slot_p[slot * a.E + e] = p;
-            a.slot_c[slot * a.E + e] = hist[e];
+            dst_p[e] = p;
+            dst_c[e] = hist[e];
             hist[e] = 0;
         }
         if (threadIdx.x == 0) {
-            a.slot_n[slot] = s_n;
+            (CL ? own_n : a.slot_n)[slot] = s_n;
             s_n = 0;
         }
         __syncthreads();
+    }
+    feed.drain();
+    if constexpr (CL) {
+        __shared__ float s_dot[kBalWarps];
+        const int rank = blockIdx.x, ranks = gridDim.x;
+        cluster_sync_all();
+        for (int q = rank; q < a.Q; q += ranks) {
+            int n = 0;
+            for (int r = 0; r < ranks; ++r) n += __float_as_int(ld_cluster_f32(reinterpret_cast<const float*>(own_n + q), r));
+            float dot = 0.0f;
+            for (int e = threadIdx.x; e < a.E; e += blockDim.x) {
+                float p = 0.0f;
+                int c = 0;
+#pragma unroll
+                for (int r = 0; r < kBalCluster; ++r) {
+                    p += ld_cluster_f32(own_p + q * a.E + e, r);
+                    c += __float_as_int(ld_cluster_f32(reinterpret_cast<const float*>(own_c + q * a.E + e), r));
+                }
+                a.prob_sums[static_cast<size_t>(q) * a.E + e] = p;
+                a.counts[static_cast<size_t>(q) * a.E + e] = c;
+                dot += static_cast<float>(c) * p;
+            }
+            dot = warp_tree_sum(n > 0 ? dot : 0.0f);
+            if (lane == 0) s_dot[warp] = dot;
+            __syncthreads();
+            if (threadIdx.x == 0) {
+                for (int w = 1; w < static_cast<int>(blockDim.x) / 32; ++w) dot += s_dot[w];
+                const float fn = static_cast<float>(n);
+                st_cluster(own_l + q, 0, n > 0 ? dot * (static_cast<float>(a.E) / static_cast<float>(a.k)) / fn / fn : 0.0f);
+                st_cluster(reinterpret_cast<float*>(own_n) + a.Q * 2 + q, 0, __int_as_float(n > 0));
+                a.seq_tokens[q] = n;
+            }
+            __syncthreads();
+        }
+        cluster_sync_all();      // also keeps every CTA's shared memory until its readers are done
+        if (rank == 0 && threadIdx.x == 0) {
+            double l = 0.0;
+            int some = 0;
+            for (int q = 0; q < a.Q; ++q) l += own_l[q], some += own_n[2 * a.Q + q];
+            a.loss[0] = static_cast<float>(l * a.coeff / (some > 0 ? some : 1));
+        }
     }
 }
 
@@ -373,197 +589,291 @@ __global__ void __launch_bounds__(kFinExperts * kFinLanes) balance_finish_kernel
     }
 }
 
+// What a row's picks get from the gate's own gradient: lane j's pick `id` (-1:
+// none) with logit xj and incoming gradient dw.
+__device__ __forceinline__ float gate_pick_grad(int id, float xj, float dw) {
+    const float u = ex2_approx(fabsf(xj) * -kLog2e), r = rcp_approx(1.0f + u);
+    float s = id < 0 ? 0.0f : xj >= 0.0f ? r : u * r;
+    float tot = warp_tree_sum(s);
+    if (tot < kBalTinySum) {      // relative to the largest, as the rows of the loss
+        const float m = warp_max(id >= 0 ? xj : -INFINITY);
+        s = id < 0 || xj == -INFINITY ? 0.0f : ex2_approx((xj - m) * kLog2e);
+        tot = warp_tree_sum(s);
+    }
+    // divided: a token's only pick has the weight 1 and no gradient
+    const float w = tot == 0.0f ? 0.0f : __fdiv_rn(s, tot);
+    const float dot = warp_tree_sum(dw * w);
+    float d = w * (xj >= 0.0f ? u * r : r) * (dw - dot);
+    const unsigned same = __match_any_sync(0xffffffffu, id);
+    if (__any_sync(0xffffffffu, id >= 0 && __popc(same) > 1)) {   // the same expert twice: added in slot order
+        float z = 0.0f;
+        for (int j = 0; j < 32; ++j) {
+            const float dj = __shfl_sync(0xffffffffu, d, j);
+            if (same >> j & 1u) z += dj;
+        }
+        d = z;
+    }
+    return d;
+}
+
 // The gradient of the logits.  A team keeps its row in registers; the few
 // entries of the gate's own gradient are laid into a row of shared memory
 // (zero elsewhere) that the dense pass adds, so every logit's gradient is
-// written once, in full lines.
+// written once, in full lines.  In a team of several warps they take turns at
+// the gate: warp i % W forms row i's entries while the others are a row behind
+// (three such rows in turn: being cleared, read and filled); a warp alone needs
+// one.  Picks are fetched two turns ahead, their logits and gradients one.
 template <int NV, bool VEC, bool BAL>
-__global__ void __launch_bounds__(kBalWarps * 32) gate_grad_kernel(const BalArgs a) {
+__global__ void __launch_bounds__(kBalWarps * 32, 1) gate_grad_kernel(const BalArgs a) {
     constexpr int NE = 4 * NV;
-    extern __shared__ __align__(16) uint8_t bal_smem[];
+    extern __shared__ __align__(128) uint8_t bal_smem[];
     __shared__ float2 red[kBalWarps][2 * kBalMaxTeam];
+    __shared__ __align__(8) uint64_t bars[kBalWarps * kBalRing];
+    __shared__ int s_some;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int team = warp / a.W;
-    const int pitch = (a.E + 3) & ~3;
-    float* add0 = reinterpret_cast<float*>(bal_smem) + static_cast<size_t>(team) * 2 * pitch;   // two rows per team
+    const int pitch = (a.E + 3) & ~3, bufs = a.W == 1 ? 1 : 3;
+    float* adds = reinterpret_cast<float*>(bal_smem + (BAL ? bal_ring_bytes<NV>(a.W * a.teams, a.ring) : 0));
+    float* add0 = adds + static_cast<size_t>(team) * bufs * pitch;
     Team tm{red[team], a.W, 1 + team, warp % a.W, lane, 0};
-    const int64_t t0 = static_cast<int64_t>(blockIdx.x) * a.tokens;
-    const int t1 = static_cast<int>(min(t0 + a.tokens, static_cast<int64_t>(a.T)));
-    for (int e = threadIdx.x; e < a.teams * 2 * pitch; e += blockDim.x) reinterpret_cast<float*>(bal_smem)[e] = 0.0f;
+    const int64_t c0 = static_cast<int64_t>(blockIdx.x) * a.tokens;
+    const int t0 = static_cast<int>(min(c0, static_cast<int64_t>(a.T)));
+    const int t1 = static_cast<int>(min(c0 + a.tokens, static_cast<int64_t>(a.T)));
+    for (int e = threadIdx.x; e < a.teams * bufs * pitch; e += blockDim.x) adds[e] = 0.0f;
+    for (int i = threadIdx.x; i < kBalWarps * kBalRing; i += blockDim.x) mbar_init(&bars[i], 1);
+    if (threadIdx.x == 0) s_some = 0;
+    fence_mbar_init();
+    __syncthreads();
     griddep_wait();
     griddep_launch();
+    RowFeed<NV, VEC> feed;
+    RowMask mask;
+    mask.start(a, lane, t0 + team, t1);
     float unit = 0.0f;
     if constexpr (BAL) {
-        __shared__ int s_some;
-        if (threadIdx.x == 0) s_some = 0;
-        __syncthreads();
+        feed.start(a, tm, warp, t0 + team, t1, bal_smem, bars);
         int some = 0;
         for (int q = threadIdx.x; q < a.Q; q += blockDim.x) some += a.seq_tokens_in[q] > 0;
         if (some) atomicAdd(&s_some, some);
         __syncthreads();
         unit = a.grad_loss[0] * a.coeff * (static_cast<float>(a.E) / static_cast<float>(a.k)) /
                static_cast<float>(s_some > 0 ? s_some : 1);
-    } else {
-        __syncthreads();
     }
 
-    int q = BAL ? first_sequence(a, static_cast<int>(t0)) : a.Q;
-    int q_of_g = -1;
-    float g[NE];
+    int q = BAL ? first_sequence(a, t0) : a.Q, q_lo = 0, q_hi = -1;
+    float2 g[NE / 2];
 #pragma unroll
-    for (int i = 0; i < NE; ++i) g[i] = 0.0f;
-    int old_id = -1;
-    int par = 0;
-    for (int t = static_cast<int>(t0) + team; t < t1; t += a.teams, par ^= 1) {
-        float* add = add0 + par * pitch;
-        const bool valid = a.mask[t] != 0;
+    for (int i = 0; i < NE / 2; ++i) g[i] = make_float2(0.0f, 0.0f);
+
+    // this warp's turns at the gate: rows wt, wt + W, ... of the team
+    const bool gate = a.grad_w != nullptr;
+    const int turn = a.W * a.teams;
+    int tg = t0 + team + tm.wt * a.teams;          // token of this warp's next turn
+    // what a fetch leaves is only looked at a turn later, so no load is waited for where it starts
+    auto fetch_pick = [&](int64_t t, int& d, int& m) {
+        d = -1, m = 0;
+        if (gate && t < t1 && lane < a.k) {
+            d = a.ids[static_cast<size_t>(t) * a.k + lane];
+            m = a.mask[t];
+        }
+    };
+    auto picked = [&](int d, int m) { return m != 0 && d >= 0 && d < a.E ? d : -1; };   // -1: none
+    auto fetch_values = [&](int64_t t, int d, float& x, float& w) {
+        x = 0.0f, w = 0.0f;
+        if (d >= 0) {
+            x = a.logits[static_cast<size_t>(t) * a.E + d];
+            w = a.grad_w[static_cast<size_t>(t) * a.k + lane];
+        }
+    };
+    int id, id1, m1;
+    float xj, dw;
+    fetch_pick(tg, id, m1);
+    id = picked(id, m1);
+    fetch_values(tg, id, xj, dw);
+    fetch_pick(static_cast<int64_t>(tg) + turn, id1, m1);
+    int old_id = -1;                // this lane's entry of the warp's last turn, not yet cleared
+    float* old_buf = add0;
+    auto take_turn = [&](int buf) {
+        int id2, m2;
+        float xj1, dw1;
+        id1 = picked(id1, m1);
+        fetch_pick(static_cast<int64_t>(tg) + 2 * static_cast<int64_t>(turn), id2, m2);
+        fetch_values(static_cast<int64_t>(tg) + turn, id1, xj1, dw1);
+        if (__any_sync(0xffffffffu, id >= 0)) {
+            const float d = gate_pick_grad(id, xj, dw);
+            __syncwarp();       // behind the lanes that cleared this buffer
+            if (id >= 0) add0[buf * pitch + id] = d;
+        }
+        old_id = id, old_buf = add0 + buf * pitch;
+        id = id1, id1 = id2, m1 = m2, xj = xj1, dw = dw1;
+        tg += turn;
+    };
+
+    int row = 0, rbuf = 0, whose = 0;      // row of the team, its buffer, and the warp whose turn it was
+    if (gate && a.W > 1 && tm.wt == 0 && t0 + team < t1) take_turn(0);
+    for (int t = t0 + team; t < t1; t += a.teams, ++row) {
+        const bool valid = mask.next();
         bool in_seq = false;
-        float x[NE];
+        float2 x[NE / 2];
         if constexpr (BAL) {
-            if (valid) {
-                bal_load<NV, VEC>(a.logits + static_cast<size_t>(t) * a.E, a.E, tm.wt, lane, x);
-                while (q < a.Q && clamp_offset(a, q + 1) <= t) ++q;
-                in_seq = q < a.Q && clamp_offset(a, q) <= t;
-                if (in_seq && q != q_of_g) {
-                    q_of_g = q;
-                    const int n = a.seq_tokens_in[q];
-                    const float fn = static_cast<float>(n);
-                    const float c = n > 0 ? unit / fn / fn : 0.0f;
+            feed.take(x);
+            if (t >= q_hi) {
+                while (q < a.Q && (q_hi = clamp_offset(a, q + 1)) <= t) ++q;
+                if (q >= a.Q) q_hi = a.T;
+                q_lo = q < a.Q ? clamp_offset(a, q) : a.T;
+                const int n = q < a.Q ? a.seq_tokens_in[q] : 0;
+                const float fn = static_cast<float>(n);
+                const float c = n > 0 ? unit / fn / fn : 0.0f;
+                const int32_t* row_c = a.counts_in + static_cast<size_t>(q < a.Q ? q : 0) * a.E;
 #pragma unroll
-                    for (int i = 0; i < NE; ++i) {
-                        const int e = bal_expert<NV, VEC>(tm.wt, lane, i);
-                        g[i] = e < a.E ? c * static_cast<float>(a.counts_in[static_cast<size_t>(q) * a.E + e]) : 0.0f;
-                    }
+                for (int i = 0; i < NE / 2; ++i) {
+                    const int e0 = bal_expert<NV, VEC>(tm.wt, lane, 2 * i), e1 = bal_expert<NV, VEC>(tm.wt, lane, 2 * i + 1);
+                    g[i].x = e0 < a.E ? c * static_cast<float>(row_c[e0]) : 0.0f;
+                    g[i].y = e1 < a.E ? c * static_cast<float>(row_c[e1]) : 0.0f;
                 }
             }
+            in_seq = valid && t >= q_lo;
         }
-        // the gate's own gradient: one pick per lane
-        int id = -1;
-        if (tm.wt == 0 && a.grad_w != nullptr && valid) {
-            float xj = -INFINITY, dw = 0.0f;
-            if (lane < a.k) {
-                id = a.ids[static_cast<size_t>(t) * a.k + lane];
-                if (id < 0 || id >= a.E) id = -1;
-                if (id >= 0) {
-                    xj = a.logits[static_cast<size_t>(t) * a.E + id];
-                    dw = a.grad_w[static_cast<size_t>(t) * a.k + lane];
-                }
-            }
-            const float m = fminf(warp_max(xj), 0.0f);
-            const float u = expf(-fabsf(xj)), r = __frcp_rn(1.0f + u);
-            // s exp(-m): sigmoids relative to the largest, 1 - s from the same two
-            const float sj = xj == -INFINITY ? 0.0f : expf(fminf(xj, 0.0f) - m) * r;
-            const float tot = warp_tree_sum(sj);
-            const float w = tot == 0.0f ? 0.0f : __fdiv_rn(sj, tot);
-            const float dot = warp_tree_sum(dw * w);
-            float d = w * (xj >= 0.0f ? u * r : r) * (dw - dot);
-            const unsigned same = __match_any_sync(0xffffffffu, id);
-            if (__any_sync(0xffffffffu, id >= 0 && __popc(same) > 1)) {   // the same expert twice: added in slot order
-                float z = 0.0f;
-                for (int j = 0; j < 32; ++j) {
-                    const float dj = __shfl_sync(0xffffffffu, d, j);
-                    if (same >> j & 1u) z += dj;
-                }
-                d = z;
-            }
-            __syncwarp();   // behind the lanes that cleared this buffer
-            if (id >= 0) add[id] = d;
-        }
-        float S = 0.0f, G = 0.0f;
-        float sl[NE];
+        if (gate && a.W == 1) take_turn(0);
+        float2 S2 = make_float2(0.0f, 0.0f), G2 = S2;
         if (BAL && in_seq) {
-            float2 loc = make_float2(0.0f, 0.0f);
+            float2 sum = make_float2(0.0f, 0.0f), dot = sum;
+            float2 keep[NE / 2];
 #pragma unroll
-            for (int i = 0; i < NE; ++i) {
-                const float u = ex2_approx(fabsf(x[i]) * -kLog2e), r = rcp_approx(1.0f + u), ur = u * r;
-                const float s = x[i] >= 0.0f ? r : ur;
-                sl[i] = ur * r;
-                loc.x += s;
-                loc.y = fmaf(g[i], s, loc.y);
+            for (int i = 0; i < NE / 2; ++i) {
+                const float2 u = make_float2(ex2_approx(fabsf(x[i].x) * -kLog2e), ex2_approx(fabsf(x[i].y) * -kLog2e));
+                const float2 d = add2(u, make_float2(1.0f, 1.0f));
+                const float2 r = make_float2(rcp_approx(d.x), rcp_approx(d.y));
+                const float2 ur = mul2(u, r);
+                const float2 s = make_float2(x[i].x >= 0.0f ? r.x : ur.x, x[i].y >= 0.0f ? r.y : ur.y);
+                keep[i] = mul2(ur, r);
+                sum = add2(sum, s);
+                dot = fma2(g[i], s, dot);
             }
-            loc = tm.sum(loc);
-            if (loc.x < kBalTinySum) {
+            float2 all = tm.sum(make_float2(sum.x + sum.y, dot.x + dot.y));
+            if (all.x < kBalTinySum) {
                 float m = -INFINITY;
 #pragma unroll
-                for (int i = 0; i < NE; ++i) m = fmaxf(m, x[i]);
+                for (int i = 0; i < NE / 2; ++i) m = fmaxf(m, fmaxf(x[i].x, x[i].y));
                 m = tm.max(m);
-                loc = make_float2(0.0f, 0.0f);
+                sum = dot = make_float2(0.0f, 0.0f);
 #pragma unroll
-                for (int i = 0; i < NE; ++i) {
-                    sl[i] = m == -INFINITY ? 0.0f : ex2_approx((x[i] - m) * kLog2e);
-                    loc.x += sl[i];
-                    loc.y = fmaf(g[i], sl[i], loc.y);
+                for (int i = 0; i < NE / 2; ++i) {
+                    keep[i] = m == -INFINITY ? make_float2(0.0f, 0.0f)
+                                             : make_float2(ex2_approx((x[i].x - m) * kLog2e), ex2_approx((x[i].y - m) * kLog2e));
+                    sum = add2(sum, keep[i]);
+                    dot = fma2(g[i], keep[i], dot);
                 }
-                loc = tm.sum(loc);
+                all = tm.sum(make_float2(sum.x + sum.y, dot.x + dot.y));
             }
-            S = loc.x == 0.0f ? 0.0f : __frcp_rn(loc.x);
-            G = loc.y * S;
+#pragma unroll
+            for (int i = 0; i < NE / 2; ++i) x[i] = keep[i];
+            const float S = all.x == 0.0f ? 0.0f : __frcp_rn(all.x);
+            const float G = all.y * S;
+            S2 = make_float2(S, S), G2 = make_float2(-G, -G);
         } else {
-            tm.sum(0.0f);   // the barrier that makes `add` visible to the team
+            tm.sync();      // makes the row's entries visible to the team
+#pragma unroll
+            for (int i = 0; i < NE / 2; ++i) x[i] = make_float2(0.0f, 0.0f);
         }
-        // the previous row's entries: every warp has read them by now
-        if (old_id >= 0) (add0 + (par ^ 1) * pitch)[old_id] = 0.0f;
-        old_id = id;
-        float* row = a.grad + static_cast<size_t>(t) * a.E;
+        const float* add = add0 + rbuf * pitch;
+        float* out = a.grad + static_cast<size_t>(t) * a.E;
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
-            float d[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) d[i] = BAL && in_seq ? (g[4 * v + i] - G) * (sl[4 * v + i] * S) : 0.0f;
+            const float2 lo = mul2(mul2(x[2 * v], S2), add2(g[2 * v], G2));
+            const float2 hi = mul2(mul2(x[2 * v + 1], S2), add2(g[2 * v + 1], G2));
             if constexpr (VEC) {
                 const int e = bal_expert<NV, VEC>(tm.wt, lane, 4 * v);
                 if (e < a.E) {
                     const float4 z = *reinterpret_cast<const float4*>(add + e);
-                    __stcs(reinterpret_cast<float4*>(row + e),
-                           make_float4(d[0] + z.x, d[1] + z.y, d[2] + z.z, d[3] + z.w));
+                    const float2 p = add2(lo, make_float2(z.x, z.y)), r = add2(hi, make_float2(z.z, z.w));
+                    __stcs(reinterpret_cast<float4*>(out + e), make_float4(p.x, p.y, r.x, r.y));
                 }
             } else {
+                const float w[4] = {lo.x, lo.y, hi.x, hi.y};
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int e = bal_expert<NV, VEC>(tm.wt, lane, 4 * v + i);
-                    if (e < a.E) __stcs(row + e, d[i] + add[e]);
+                    if (e < a.E) __stcs(out + e, w[i] + add[e]);
                 }
             }
         }
+        if (a.W == 1) {
+            __syncwarp();
+            if (old_id >= 0) old_buf[old_id] = 0.0f;
+        } else if (gate) {
+            // The warp that formed the row before this one clears it: at this row's barrier every warp had read it.
+            // The next warp in turn fills the row behind this one; its buffer was cleared a row ago.
+            const int next_buf = rbuf == 2 ? 0 : rbuf + 1;
+            const int prev = whose == 0 ? a.W - 1 : whose - 1, then = whose == a.W - 1 ? 0 : whose + 1;
+            if (tm.wt == prev && row > 0) {
+                if (old_id >= 0) old_buf[old_id] = 0.0f;
+                old_id = -1;
+            }
+            if (tm.wt == then && t + a.teams < t1) take_turn(next_buf);
+            rbuf = next_buf, whose = then;
+        }
     }
+    if constexpr (BAL) feed.drain();
 }
 
 template <typename F>
-cudaError_t bal_launch(F* kernel, const BalPlan& p, size_t smem, const BalArgs& a, cudaStream_t s) {
-    if (smem > 48 * 1024) {
+cudaError_t bal_launch(F* kernel, int ctas, int threads, size_t smem, int cluster, const BalArgs& a, cudaStream_t s) {
+    if (smem > 40 * 1024) {      // with the kernel's static shared memory above the 48 KB of an unset limit
         const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel),
                                                    cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
         if (e != cudaSuccess) return e;
     }
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(p.ctas);
-    cfg.blockDim = dim3(p.W * p.teams * 32);
+    cfg.gridDim = dim3(ctas);
+    cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
+    if (cluster > 1) {
+        attr[1].id = cudaLaunchAttributeClusterDimension;
+        attr[1].val.clusterDim.x = cluster;
+        attr[1].val.clusterDim.y = 1;
+        attr[1].val.clusterDim.z = 1;
+        cfg.numAttrs = 2;
+    }
     return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
+template <int NV, bool VEC>
+cudaError_t launch_balance_nv(const BalPlan& p, const BalArgs& a, cudaStream_t s) {
+    const int warps = p.W * p.teams;
+    size_t smem = bal_ring_bytes<NV>(warps, p.ring) + static_cast<size_t>(p.teams + 1) * a.E * 4;
+    if (!p.cluster) return bal_launch(balance_kernel<NV, VEC, false>, p.ctas, warps * 32, smem, 1, a, s);
+    smem += static_cast<size_t>(a.Q) * (2 * a.E + 3) * 4;
+    return bal_launch(balance_kernel<NV, VEC, true>, kBalCluster, warps * 32, smem, kBalCluster, a, s);
+}
 template <bool VEC>
-cudaError_t launch_balance_main(const BalPlan& p, size_t smem, const BalArgs& a, cudaStream_t s) {
+cudaError_t launch_balance_main(const BalPlan& p, const BalArgs& a, cudaStream_t s) {
     switch (p.nv) {
-        case 1: return bal_launch(balance_kernel<1, VEC>, p, smem, a, s);
-        case 2: return bal_launch(balance_kernel<2, VEC>, p, smem, a, s);
-        case 3: return bal_launch(balance_kernel<3, VEC>, p, smem, a, s);
-        default: return bal_launch(balance_kernel<4, VEC>, p, smem, a, s);
+        case 1: return launch_balance_nv<1, VEC>(p, a, s);
+        case 2: return launch_balance_nv<2, VEC>(p, a, s);
+        case 3: return launch_balance_nv<3, VEC>(p, a, s);
+        default: return launch_balance_nv<4, VEC>(p, a, s);
     }
 }
+template <int NV, bool VEC, bool BAL>
+cudaError_t launch_gate_grad_nv(const BalPlan& p, const BalArgs& a, cudaStream_t s) {
+    const int warps = p.W * p.teams;
+    const size_t smem = (BAL ? bal_ring_bytes<NV>(warps, p.ring) : 0) + static_cast<size_t>(p.teams) * (p.W == 1 ? 1 : 3) * ((a.E + 3) & ~3) * 4;
+    return bal_launch(gate_grad_kernel<NV, VEC, BAL>, p.ctas, warps * 32, smem, 1, a, s);
+}
 template <bool VEC, bool BAL>
-cudaError_t launch_gate_grad(const BalPlan& p, size_t smem, const BalArgs& a, cudaStream_t s) {
+cudaError_t launch_gate_grad(const BalPlan& p, const BalArgs& a, cudaStream_t s) {
     switch (p.nv) {
-        case 1: return bal_launch(gate_grad_kernel<1, VEC, BAL>, p, smem, a, s);
-        case 2: return bal_launch(gate_grad_kernel<2, VEC, BAL>, p, smem, a, s);
-        case 3: return bal_launch(gate_grad_kernel<3, VEC, BAL>, p, smem, a, s);
-        default: return bal_launch(gate_grad_kernel<4, VEC, BAL>, p, smem, a, s);
+        case 1: return launch_gate_grad_nv<1, VEC, BAL>(p, a, s);
+        case 2: return launch_gate_grad_nv<2, VEC, BAL>(p, a, s);
+        case 3: return launch_gate_grad_nv<3, VEC, BAL>(p, a, s);
+        default: return launch_gate_grad_nv<4, VEC, BAL>(p, a, s);
     }
 }
 
@@ -573,27 +883,30 @@ int bal_parts(int E) { return (E + kFinExperts - 1) / kFinExperts; }
 }  // namespace
 
 size_t balance_workspace_bytes(int T, int E, int Q) {
-    const size_t slots = static_cast<size_t>(bal_plan(T, E).ctas) + Q;
+    const BalPlan p = bal_plan(T, E, Q);
+    if (p.cluster) return 0;
+    const size_t slots = static_cast<size_t>(p.ctas) + Q;
     return 16 + 2 * pad16(slots * E * 4) + pad16(slots * 4) + pad16(static_cast<size_t>(Q) * bal_parts(E) * 4);
 }
 
 cudaError_t launch_balance_loss(const BalanceLaunch& b, cudaStream_t s) {
-    const BalPlan p = bal_plan(b.T, b.E);
+    const BalPlan p = bal_plan(b.T, b.E, b.Q);
     BalArgs a{};
     a.logits = b.logits, a.ids = b.ids, a.mask = b.mask, a.offsets = b.offsets;
     a.T = b.T, a.E = b.E, a.k = b.k, a.Q = b.Q, a.coeff = b.coeff;
-    a.W = p.W, a.teams = p.teams, a.tokens = p.tokens;
-    const size_t slots = static_cast<size_t>(p.ctas) + b.Q;
-    uint8_t* w = static_cast<uint8_t*>(b.workspace);
-    a.ticket = reinterpret_cast<unsigned int*>(w);
-    a.slot_p = reinterpret_cast<float*>(w += 16);
-    a.slot_c = reinterpret_cast<int32_t*>(w += pad16(slots * b.E * 4));
-    a.slot_n = reinterpret_cast<int32_t*>(w += pad16(slots * b.E * 4));
-    a.loss_part = reinterpret_cast<float*>(w += pad16(slots * 4));
+    a.W = p.W, a.teams = p.teams, a.tokens = p.tokens, a.ring = p.ring;
     a.loss = b.loss, a.counts = b.counts, a.prob_sums = b.prob_sums, a.seq_tokens = b.seq_tokens;
-    const size_t smem = static_cast<size_t>(p.teams + 1) * b.E * 4;
-    cudaError_t e = b.E % 4 == 0 ? launch_balance_main<true>(p, smem, a, s) : launch_balance_main<false>(p, smem, a, s);
-    if (e != cudaSuccess) return e;
+    if (!p.cluster) {
+        const size_t slots = static_cast<size_t>(p.ctas) + b.Q;
+        uint8_t* w = static_cast<uint8_t*>(b.workspace);
+        a.ticket = reinterpret_cast<unsigned int*>(w);
+        a.slot_p = reinterpret_cast<float*>(w += 16);
+        a.slot_c = reinterpret_cast<int32_t*>(w += pad16(slots * b.E * 4));
+        a.slot_n = reinterpret_cast<int32_t*>(w += pad16(slots * b.E * 4));
+        a.loss_part = reinterpret_cast<float*>(w += pad16(slots * 4));
+    }
+    const cudaError_t e = b.E % 4 == 0 ? launch_balance_main<true>(p, a, s) : launch_balance_main<false>(p, a, s);
+    if (e != cudaSuccess || p.cluster) return e;
     const int parts = bal_parts(b.E);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(parts, b.Q < 65535 ? b.Q : 65535);
@@ -608,17 +921,16 @@ cudaError_t launch_balance_loss(const BalanceLaunch& b, cudaStream_t s) {
 }
 
 cudaError_t launch_route_backward(const GateGradLaunch& b, cudaStream_t s) {
-    const BalPlan p = bal_plan(b.T, b.E);
+    const BalPlan p = bal_plan(b.T, b.E, kBalClusterSums);    // never the cluster's split
     BalArgs a{};
     a.logits = b.logits, a.ids = b.ids, a.mask = b.mask, a.offsets = b.offsets;
     a.T = b.T, a.E = b.E, a.k = b.k, a.Q = b.Q, a.coeff = b.coeff;
-    a.W = p.W, a.teams = p.teams, a.tokens = p.tokens;
+    a.W = p.W, a.teams = p.teams, a.tokens = p.tokens, a.ring = p.ring;
     a.grad_w = b.grad_w, a.grad_loss = b.grad_loss, a.counts_in = b.counts, a.seq_tokens_in = b.seq_tokens;
     a.grad = b.grad;
-    const size_t smem = static_cast<size_t>(p.teams) * 2 * ((b.E + 3) & ~3) * 4;
     const bool bal = b.grad_loss != nullptr;
-    if (b.E % 4 == 0) return bal ? launch_gate_grad<true, true>(p, smem, a, s) : launch_gate_grad<true, false>(p, smem, a, s);
-    return bal ? launch_gate_grad<false, true>(p, smem, a, s) : launch_gate_grad<false, false>(p, smem, a, s);
+    if (b.E % 4 == 0) return bal ? launch_gate_grad<true, true>(p, a, s) : launch_gate_grad<true, false>(p, a, s);
+    return bal ? launch_gate_grad<false, true>(p, a, s) : launch_gate_grad<false, false>(p, a, s);
 }
 
 }  // namespace mb

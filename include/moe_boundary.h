@@ -254,8 +254,9 @@ int expert_combine_join(const uint16_t* expert_out, int64_t num_rows, int H, con
  *   loss        [1] FP32 (out)      counts      [Q, E] int32 (out)
  *   prob_sums   [Q, E] FP32 (out)   seq_tokens  [Q] int32 (out)
  *   workspace   device scratch of moe_balance_workspace_size(T, E, Q) bytes,
- *               16-byte aligned; needs no initialisation; two calls that
- *               overlap on the GPU need two
+ *               16-byte aligned (may be NULL when that size is 0: small
+ *               batches); needs no initialisation; two calls that overlap on
+ *               the GPU need two
  * Sums are FP32 in an order fixed by the sizes (no floating-point atomics).
  * Offsets that are not ascending give undefined outputs, never an access out
  * of bounds.  T == 0 writes zeros (topk_ids, logits and token_mask may then be
@@ -543,7 +544,8 @@ const char* mb_last_error(void);
  * consumer's wait for a copied row ran out; bit 3: the router projection's
  * wait for its tensor-core MMAs ran out; bit 4: the finalize all-reduce's
  * wait for a peer's partial ran out; bit 5: a wait inside the low-rank adapters'
- * tensor-core kernels ran out.  0 means no kernel reported a
+ * tensor-core kernels ran out; bit 6: the router training kernels' wait for a
+ * copied row ran out.  0 means no kernel reported a
  * timeout since the last call.  Returns -1 (and sets mb_last_error) when the
  * CUDA runtime fails.
  */

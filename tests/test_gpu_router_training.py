@@ -85,6 +85,42 @@ def test_long_batches_cut_anywhere(cuda_dev):
     _check(cuda_dev, x[:, :9], np.clip(ids, -1, 9), mask, dw)    # id 9: outside E = 9
 
 
+@pytest.mark.parametrize("T,E,k,off", [(5000, 64, 6, [0, 1, 1, 40, 41, 2500, 4990]), (5001, 66, 6, [3, 2049, 5001]),
+                                       (300, 1000, 8, [0, 17, 150, 299]), (130, 2560, 8, [1, 64, 65, 130]),
+                                       (90, 4096, 32, None), (88, 3001, 8, [0, 44, 88]), (40, 2560, 4, [0, 7, 8, 40]),
+                                       (600, 512, 22, None)])
+def test_batches_of_many_ctas(cuda_dev, T, E, k, off):
+    """Sums that pass through slots of several CTAs, or more sums than a cluster's shared memory is used for."""
+    assert eb.balance_workspace_size(T, E, 1 if off is None else len(off) - 1) > 0
+    _check(cuda_dev, *_inputs(T, E, k, seed=T + E), off=off)
+
+
+def test_more_tokens_than_one_wave(cuda_dev):
+    """Past 64 rows for each of the card's teams: more CTAs than SMs, against sums in binary64 on the GPU."""
+    T, E, k = 160000, 16, 2
+    g = torch.Generator(device=cuda_dev).manual_seed(5)
+    x = torch.randn(T, E, generator=g, device=cuda_dev)
+    mask = (torch.rand(T, generator=g, device=cuda_dev) > 0.1).to(torch.uint8)
+    ids = torch.topk(x, k, dim=1).indices.to(torch.int32)
+    loss, counts, probs, n = eb.moe_balance_loss(x, ids, mask, 0.1)
+    s = torch.sigmoid(x.double())
+    p = s / s.sum(1, keepdim=True) * mask.double()[:, None]
+    want = p.sum(0)
+    assert int(n) == int(mask.sum())
+    assert torch.equal(counts[0].long(), torch.bincount(ids[mask != 0].flatten().long(), minlength=E))
+    tol = (float(x.abs().max()) + 40 + 72 + T / 128 + 16) * U
+    assert bool(((probs[0].double() - want).abs() <= tol * want).all())
+    wl = 0.1 * E / (k * float(n) ** 2) * float((counts[0].double() * want).sum())
+    assert abs(float(loss) - wl) <= (tol + 20 * U) * wl
+    dw = torch.randn(T, k, generator=g, device=cuda_dev)
+    got = eb.moe_route_backward(x, ids, mask, grad_weights=dw)
+    sj = torch.gather(s, 1, ids.long())
+    w = sj / sj.sum(1, keepdim=True)
+    part = w * (1 - sj) * (dw.double() - (dw.double() * w).sum(1, keepdim=True)) * mask.double()[:, None]
+    ref = torch.zeros_like(s).scatter_add_(1, ids.long(), part)
+    assert float((got.double() - ref).norm() / ref.norm()) < 60 * U
+
+
 def test_every_token_masked(cuda_dev):
     x, ids, mask, dw = _inputs(20, 40, 4, seed=1)
     mask[:] = 0
@@ -150,6 +186,7 @@ def test_repeats_bit_for_bit_and_leaves_guards(cuda_dev):
     out["counts"], out["prob_sums"] = out["counts"].view(Q, E), out["prob_sums"].view(Q, E)
     out["grad"] = out["grad"].view(T, E)
     need = eb.balance_workspace_size(T, E, Q)
+    assert need > 0
     ws = torch.full((need + 256,), 77, dtype=torch.uint8, device=cuda_dev)
     one = torch.ones(1, device=cuda_dev)
 

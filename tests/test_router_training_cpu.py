@@ -81,9 +81,12 @@ def test_library_refuses_before_any_launch():
     assert loss(Q=3) == 1 and "seq_offsets" in eb.last_error()
     assert loss(ptr=N) == 1 and "null" in eb.last_error()
     assert loss(out=N) == 1 and loss(out=odd) == 1 and loss(ptr=odd) == 1 and loss(off=odd, Q=2) == 1
-    assert loss(ws=N) == 1 and "workspace" in eb.last_error()
-    need = eb.balance_workspace_size(4, 16, 1)
-    assert need > 0 and loss(size=ctypes.c_size_t(need - 1)) == 1 and loss(size=Z) == 1 and loss(ws=odd) == 1
+    T = 100000                                                  # a batch that needs a workspace
+    assert loss(T=T, ws=N) == 1 and "workspace" in eb.last_error()
+    need = eb.balance_workspace_size(T, 16, 1)
+    assert need > 0 and loss(T=T, size=ctypes.c_size_t(need - 1)) == 1 and loss(T=T, size=Z) == 1
+    assert loss(T=T, ws=odd) == 1 and "aligned" in eb.last_error()
+    assert eb.balance_workspace_size(4, 16, 1) == 0
     assert eb.balance_workspace_size(4, 5000, 1) == 0 and eb.balance_workspace_size(4, 16, 0) == 0
 
     b = ctypes.c_void_p(0x2000)
