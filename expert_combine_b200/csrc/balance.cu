@@ -43,7 +43,8 @@ namespace {
 
 constexpr int kBalLane = 16;                 // most logits per lane
 constexpr int kBalMaxTeam = kMaxExperts / (32 * kBalLane);
-constexpr int kBalWarps = 16;                // most warps of a CTA (one CTA per SM)
+constexpr int kBalWarps = 24;                // most warps of a CTA (one CTA per SM): the loss
+constexpr int kBalGradWarps = 16;            // of the gradient, which needs twice the registers, and of a cluster's CTAs
 constexpr int kBalRowsPerTeam = 128;         // most rows a team adds up in one FP32 register
 constexpr int kBalTargetCtas = 148;
 constexpr int kBalRing = 8;                  // most row slots of a warp
@@ -52,7 +53,8 @@ constexpr float kBalTinySum = 1e-20f;
 constexpr unsigned int kBalTimeout = 64u;    // bit 6 of the device status word
 constexpr int kFinExperts = 32, kFinLanes = 16;   // second kernel: experts x slot lanes per CTA
 constexpr int kBalCluster = 8;               // small batches: CTAs of the one cluster
-constexpr int kBalClusterLogits = 256 * 1024;     // T * E up to here (2 MB of logits through 8 SMs)
+constexpr int kBalClusterLogits = 256 * 1024;     // T * E up to here (1 MB of logits through 8 SMs)
+constexpr int kBalClusterRows = 32;               // rows a team takes at most
 constexpr int kBalClusterSums = 4096;             // Q * E up to here (32 KB of shared memory)
 
 struct BalPlan {
@@ -65,12 +67,14 @@ struct BalPlan {
     bool cluster; // forward pass in one cluster
 };
 
-BalPlan bal_plan(int T, int E, int Q) {
+BalPlan bal_plan(int T, int E, int Q, bool grad) {
     BalPlan p;
     p.W = (E + 32 * kBalLane - 1) / (32 * kBalLane);
-    p.teams = kBalWarps / p.W;
     p.nv = (E + 128 * p.W - 1) / (128 * p.W);
-    p.cluster = static_cast<int64_t>(T) * E <= kBalClusterLogits && static_cast<int64_t>(Q) * E <= kBalClusterSums;
+    p.cluster = !grad && T <= kBalCluster * (kBalGradWarps / p.W) * kBalClusterRows &&
+                static_cast<int64_t>(T) * E <= kBalClusterLogits && static_cast<int64_t>(Q) * E <= kBalClusterSums;
+    p.teams = (grad || p.cluster ? kBalGradWarps : kBalWarps) / p.W;
+    if (p.W > 1 && p.teams > 15) p.teams = 15;      // a team of several warps has a hardware barrier of its own, 1 .. 15
     const int64_t ctas = p.cluster ? kBalCluster : kBalTargetCtas;
     // as many rows a team as fill the card's teams, in several waves where that were more than kBalRowsPerTeam
     const int64_t per = ctas * p.teams;
@@ -131,6 +135,20 @@ __device__ __forceinline__ void st_cluster(float* local, uint32_t rank, float v)
     asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(remote), "f"(v) : "memory");
 }
 constexpr float kLog2e = 1.4426950408889634f;
+
+// Sigmoids of two logits and their slopes s (1 - s).  One reciprocal serves
+// both, 1 / a = b / (a b): with |x| the denominators are in [1, 2], so the
+// product is safe, and the special-function unit, which bounds these kernels
+// next to DRAM, has 3 results to form for a pair instead of 4.
+__device__ __forceinline__ float2 sigmoid2(float2 x, float2& slope) {
+    const float2 u = make_float2(ex2_approx(fabsf(x.x) * -kLog2e), ex2_approx(fabsf(x.y) * -kLog2e));
+    const float2 d = add2(u, make_float2(1.0f, 1.0f));
+    const float q = rcp_approx(d.x * d.y);
+    const float2 r = mul2(make_float2(q, q), make_float2(d.y, d.x));
+    const float2 ur = mul2(u, r);
+    slope = mul2(ur, r);
+    return make_float2(x.x >= 0.0f ? r.x : ur.x, x.y >= 0.0f ? r.y : ur.y);
+}
 
 // Expert of element i of this lane: groups of 4 in a row (VEC, E % 4 == 0) or
 // a stride of 32 (any E).
@@ -352,8 +370,9 @@ __host__ __device__ __forceinline__ size_t bal_ring_bytes(int warps, int ring) {
 
 // CL: one cluster of kBalCluster CTAs does all; the slots are shared memory.
 template <int NV, bool VEC, bool CL>
-__global__ void __launch_bounds__(kBalWarps * 32, 1) balance_kernel(const BalArgs a) {
+__global__ void __launch_bounds__((CL ? kBalGradWarps : kBalWarps) * 32, 1) balance_kernel(const BalArgs a) {
     constexpr int NE = 4 * NV;
+    constexpr int kWarps = CL ? kBalGradWarps : kBalWarps;
     extern __shared__ __align__(128) uint8_t bal_smem[];
     float* sums = reinterpret_cast<float*>(bal_smem + bal_ring_bytes<NV>(a.W * a.teams, a.ring));   // [teams][E]
     int32_t* hist = reinterpret_cast<int32_t*>(sums + a.teams * a.E);    // [E]
@@ -361,14 +380,14 @@ __global__ void __launch_bounds__(kBalWarps * 32, 1) balance_kernel(const BalArg
     int32_t* own_c = reinterpret_cast<int32_t*>(own_p + a.Q * a.E);      // CL: [Q][E]
     int32_t* own_n = own_c + a.Q * a.E;                                  // CL: [Q]
     float* own_l = reinterpret_cast<float*>(own_n + a.Q);                // CL: [Q] losses (rank 0)
-    __shared__ float2 red[kBalWarps][2 * kBalMaxTeam];
-    __shared__ __align__(8) uint64_t bars[kBalWarps * kBalRing];
+    __shared__ float2 red[kWarps][2 * kBalMaxTeam];
+    __shared__ __align__(8) uint64_t bars[kWarps * kBalRing];
     __shared__ int s_n;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int team = warp / a.W;
     Team tm{red[team], a.W, 1 + team, warp % a.W, lane, 0};
-    for (int i = threadIdx.x; i < kBalWarps * kBalRing; i += blockDim.x) mbar_init(&bars[i], 1);
+    for (int i = threadIdx.x; i < kWarps * kBalRing; i += blockDim.x) mbar_init(&bars[i], 1);
     for (int e = threadIdx.x; e < a.E; e += blockDim.x) hist[e] = 0;
     if (CL)
         for (int i = threadIdx.x; i < a.Q * (2 * a.E + 2); i += blockDim.x) own_c[i - a.Q * a.E] = 0;
@@ -413,9 +432,8 @@ __global__ void __launch_bounds__(kBalWarps * 32, 1) balance_kernel(const BalArg
                 float2 loc = make_float2(0.0f, 0.0f);
 #pragma unroll
                 for (int i = 0; i < NE / 2; ++i) {
-                    const float2 e = mul2(x[i], make_float2(-kLog2e, -kLog2e));
-                    const float2 d = add2(make_float2(ex2_approx(e.x), ex2_approx(e.y)), make_float2(1.0f, 1.0f));
-                    x[i] = make_float2(rcp_approx(d.x), rcp_approx(d.y));
+                    float2 slope;
+                    x[i] = sigmoid2(x[i], slope);
                     loc = add2(loc, x[i]);
                 }
                 float S = tm.sum(loc.x + loc.y);
@@ -469,7 +487,7 @@ __global__ void __launch_bounds__(kBalWarps * 32, 1) balance_kernel(const BalArg
     }
     feed.drain();
     if constexpr (CL) {
-        __shared__ float s_dot[kBalWarps];
+        __shared__ float s_dot[kWarps];
         const int rank = blockIdx.x, ranks = gridDim.x;
         cluster_sync_all();
         for (int q = rank; q < a.Q; q += ranks) {
@@ -624,11 +642,11 @@ __device__ __forceinline__ float gate_pick_grad(int id, float xj, float dw) {
 // (three such rows in turn: being cleared, read and filled); a warp alone needs
 // one.  Picks are fetched two turns ahead, their logits and gradients one.
 template <int NV, bool VEC, bool BAL>
-__global__ void __launch_bounds__(kBalWarps * 32, 1) gate_grad_kernel(const BalArgs a) {
+__global__ void __launch_bounds__(kBalGradWarps * 32, 1) gate_grad_kernel(const BalArgs a) {
     constexpr int NE = 4 * NV;
     extern __shared__ __align__(128) uint8_t bal_smem[];
-    __shared__ float2 red[kBalWarps][2 * kBalMaxTeam];
-    __shared__ __align__(8) uint64_t bars[kBalWarps * kBalRing];
+    __shared__ float2 red[kBalGradWarps][2 * kBalMaxTeam];
+    __shared__ __align__(8) uint64_t bars[kBalGradWarps * kBalRing];
     __shared__ int s_some;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int team = warp / a.W;
@@ -640,7 +658,7 @@ __global__ void __launch_bounds__(kBalWarps * 32, 1) gate_grad_kernel(const BalA
     const int t0 = static_cast<int>(min(c0, static_cast<int64_t>(a.T)));
     const int t1 = static_cast<int>(min(c0 + a.tokens, static_cast<int64_t>(a.T)));
     for (int e = threadIdx.x; e < a.teams * bufs * pitch; e += blockDim.x) adds[e] = 0.0f;
-    for (int i = threadIdx.x; i < kBalWarps * kBalRing; i += blockDim.x) mbar_init(&bars[i], 1);
+    for (int i = threadIdx.x; i < kBalGradWarps * kBalRing; i += blockDim.x) mbar_init(&bars[i], 1);
     if (threadIdx.x == 0) s_some = 0;
     fence_mbar_init();
     __syncthreads();
@@ -741,12 +759,7 @@ __global__ void __launch_bounds__(kBalWarps * 32, 1) gate_grad_kernel(const BalA
             float2 keep[NE / 2];
 #pragma unroll
             for (int i = 0; i < NE / 2; ++i) {
-                const float2 u = make_float2(ex2_approx(fabsf(x[i].x) * -kLog2e), ex2_approx(fabsf(x[i].y) * -kLog2e));
-                const float2 d = add2(u, make_float2(1.0f, 1.0f));
-                const float2 r = make_float2(rcp_approx(d.x), rcp_approx(d.y));
-                const float2 ur = mul2(u, r);
-                const float2 s = make_float2(x[i].x >= 0.0f ? r.x : ur.x, x[i].y >= 0.0f ? r.y : ur.y);
-                keep[i] = mul2(ur, r);
+                const float2 s = sigmoid2(x[i], keep[i]);
                 sum = add2(sum, s);
                 dot = fma2(g[i], s, dot);
             }
@@ -883,14 +896,14 @@ int bal_parts(int E) { return (E + kFinExperts - 1) / kFinExperts; }
 }  // namespace
 
 size_t balance_workspace_bytes(int T, int E, int Q) {
-    const BalPlan p = bal_plan(T, E, Q);
+    const BalPlan p = bal_plan(T, E, Q, false);
     if (p.cluster) return 0;
     const size_t slots = static_cast<size_t>(p.ctas) + Q;
     return 16 + 2 * pad16(slots * E * 4) + pad16(slots * 4) + pad16(static_cast<size_t>(Q) * bal_parts(E) * 4);
 }
 
 cudaError_t launch_balance_loss(const BalanceLaunch& b, cudaStream_t s) {
-    const BalPlan p = bal_plan(b.T, b.E, b.Q);
+    const BalPlan p = bal_plan(b.T, b.E, b.Q, false);
     BalArgs a{};
     a.logits = b.logits, a.ids = b.ids, a.mask = b.mask, a.offsets = b.offsets;
     a.T = b.T, a.E = b.E, a.k = b.k, a.Q = b.Q, a.coeff = b.coeff;
@@ -921,7 +934,7 @@ cudaError_t launch_balance_loss(const BalanceLaunch& b, cudaStream_t s) {
 }
 
 cudaError_t launch_route_backward(const GateGradLaunch& b, cudaStream_t s) {
-    const BalPlan p = bal_plan(b.T, b.E, kBalClusterSums);    // never the cluster's split
+    const BalPlan p = bal_plan(b.T, b.E, b.Q, true);
     BalArgs a{};
     a.logits = b.logits, a.ids = b.ids, a.mask = b.mask, a.offsets = b.offsets;
     a.T = b.T, a.E = b.E, a.k = b.k, a.Q = b.Q, a.coeff = b.coeff;

@@ -121,6 +121,12 @@ def test_more_tokens_than_one_wave(cuda_dev):
     assert float((got.double() - ref).norm() / ref.norm()) < 60 * U
 
 
+@pytest.mark.parametrize("T,E", [(4096, 8), (4097, 8), (9000, 8), (2000, 128), (2049, 128), (1024, 256), (1025, 256)])
+def test_around_the_cluster_sizes(cuda_dev, T, E):
+    """The largest batches of one cluster and the next larger ones count every token."""
+    _check(cuda_dev, *_inputs(T, E, 2, seed=T), off=[0, T // 3, T])
+
+
 def test_every_token_masked(cuda_dev):
     x, ids, mask, dw = _inputs(20, 40, 4, seed=1)
     mask[:] = 0
