@@ -21,11 +21,10 @@
 // its lane 0 starts up to 8 rows ahead, so loads need neither registers nor
 // warps in waiting (rows of E % 4 != 0 are read one ahead into registers).
 //
-// 1 - s is never formed by subtraction: with u = exp(-|x|), r = 1 / (1 + u),
-// s is r or u r by the sign of x and s (1 - s) = u r^2.  A row whose sigmoids
-// all but vanish (S < 1e-20: every logit below about -46) is scaled by its
-// largest logit first, s ~ exp(x - max), so p keeps its value as far down as
-// binary32 logits go; a row of -inf counts as p = 0.
+// 1 - s is never formed by subtraction: s (1 - s) = exp(-x) s^2.  A row whose
+// sigmoids all but vanish (S < 1e-6) or whose exponentials leave the range is
+// done over relative to its largest logit, so p keeps its value as far down as
+// binary32 logits go, and -inf (an expert shut out) has p = 0 and no gradient.
 //
 // The forward pass has no floating-point atomics: a CTA's contiguous token
 // range is cut at the sequence borders, each piece leaves its sums in a slot
@@ -49,7 +48,10 @@ constexpr int kBalRowsPerTeam = 128;         // most rows a team adds up in one 
 constexpr int kBalTargetCtas = 148;
 constexpr int kBalRing = 8;                  // most row slots of a warp
 constexpr int kBalRingBytes = 128 * 1024;    // of a CTA
-constexpr float kBalTinySum = 1e-20f;
+// A row's sigmoids are summed plainly while their sum is at least kBalTinySum.
+// What stands behind the row's end (kBalPast) adds 4e-18 a place to it.
+constexpr float kBalTinySum = 1e-6f;
+constexpr float kBalPast = -40.0f;
 constexpr unsigned int kBalTimeout = 64u;    // bit 6 of the device status word
 constexpr int kFinExperts = 32, kFinLanes = 16;   // second kernel: experts x slot lanes per CTA
 constexpr int kBalCluster = 8;               // small batches: CTAs of the one cluster
@@ -136,18 +138,29 @@ __device__ __forceinline__ void st_cluster(float* local, uint32_t rank, float v)
 }
 constexpr float kLog2e = 1.4426950408889634f;
 
-// Sigmoids of two logits and their slopes s (1 - s).  One reciprocal serves
-// both, 1 / a = b / (a b): with |x| the denominators are in [1, 2], so the
-// product is safe, and the special-function unit, which bounds these kernels
-// next to DRAM, has 3 results to form for a pair instead of 4.
-__device__ __forceinline__ float2 sigmoid2(float2 x, float2& slope) {
-    const float2 u = make_float2(ex2_approx(fabsf(x.x) * -kLog2e), ex2_approx(fabsf(x.y) * -kLog2e));
-    const float2 d = add2(u, make_float2(1.0f, 1.0f));
-    const float q = rcp_approx(d.x * d.y);
-    const float2 r = mul2(make_float2(q, q), make_float2(d.y, d.x));
-    const float2 ur = mul2(u, r);
-    slope = mul2(ur, r);
-    return make_float2(x.x >= 0.0f ? r.x : ur.x, x.y >= 0.0f ? r.y : ur.y);
+// The sigmoids of two logits, e their exponentials exp(-x).  One reciprocal
+// serves both, 1 / a = b / (a b): the special-function unit, which bounds these
+// kernels next to DRAM, forms 3 results for a pair instead of 4.  `big` grows
+// to infinity where a b leaves the range in which its reciprocal is normal (two
+// logits that add up to less than -87); the row is then done over by
+// sigmoid_over.
+__device__ __forceinline__ float2 sigmoid2(float2 x, float2& e, float& big) {
+    const float2 t = mul2(x, make_float2(-kLog2e, -kLog2e));
+    e = make_float2(ex2_approx(t.x), ex2_approx(t.y));
+    const float2 d = add2(e, make_float2(1.0f, 1.0f));
+    const float p = d.x * d.y, q = rcp_approx(p);
+    big = fmaf(p, 4.0f, big);
+    return make_float2(q * d.y, q * d.x);
+}
+
+// For any row: sigmoid(x) / exp(min(m, 0)) with m the row's largest logit, and
+// that times 1 - sigmoid(x).  With u = exp(-|x|), r = 1 / (1 + u) the sigmoid is
+// exp(min(x, 0)) r and 1 - sigmoid u r or r by the sign of x.  A row of -inf: 0.
+__device__ __forceinline__ float sigmoid_over(float x, float m, float& slope) {
+    const float u = ex2_approx(fabsf(x) * -kLog2e), r = rcp_approx(1.0f + u);
+    const float s = m == -INFINITY ? 0.0f : ex2_approx((fminf(x, 0.0f) - fminf(m, 0.0f)) * kLog2e) * r;
+    slope = s * (x >= 0.0f ? u * r : r);
+    return s;
 }
 
 // Expert of element i of this lane: groups of 4 in a row (VEC, E % 4 == 0) or
@@ -157,21 +170,21 @@ __device__ __forceinline__ int bal_expert(int wt, int lane, int i) {
     return VEC ? (wt * NV + (i >> 2)) * 128 + lane * 4 + (i & 3) : wt * NV * 128 + i * 32 + lane;
 }
 
-// One row's logits of this lane; elements past E read as -inf (sigmoid 0).
+// One row's logits of this lane; `past` stands for elements behind E.
 template <int NV, bool VEC>
-__device__ __forceinline__ void bal_load(const float* row, int E, int wt, int lane, float (&x)[4 * NV]) {
+__device__ __forceinline__ void bal_load(const float* row, int E, int wt, int lane, float past, float (&x)[4 * NV]) {
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
         if constexpr (VEC) {
             const int e = bal_expert<NV, VEC>(wt, lane, 4 * v);
-            float4 f = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+            float4 f = make_float4(past, past, past, past);
             if (e < E) f = ld_nc_f4(row + e);
             x[4 * v] = f.x, x[4 * v + 1] = f.y, x[4 * v + 2] = f.z, x[4 * v + 3] = f.w;
         } else {
 #pragma unroll
             for (int i = 4 * v; i < 4 * v + 4; ++i) {
                 const int e = bal_expert<NV, VEC>(wt, lane, i);
-                x[i] = e < E ? __ldg(row + e) : -INFINITY;
+                x[i] = e < E ? __ldg(row + e) : past;
             }
         }
     }
@@ -268,8 +281,8 @@ struct RowFeed {
             full = bars + warp * kBalRing;
             const int mine = E - wt * NV * 128;
             bytes = 4 * (mine < 0 ? 0 : mine < NV * 128 ? mine : NV * 128);
-            if (bytes < NV * 512) {     // behind the row's end the copies write nothing: -inf stays there
-                for (int i = lane; i < ring * NV * 128; i += 32) slots[i] = -INFINITY;
+            if (bytes < NV * 512) {     // behind the row's end the copies write nothing
+                for (int i = lane; i < ring * NV * 128; i += 32) slots[i] = kBalPast;
                 fence_proxy_async_smem();
                 __syncwarp();
             }
@@ -279,7 +292,7 @@ struct RowFeed {
                 advance();
             }
         } else {
-            if (left > 0) bal_load<NV, VEC>(next, E, wt, lane, ahead);
+            if (left > 0) bal_load<NV, VEC>(next, E, wt, lane, kBalPast, ahead);
         }
     }
     __device__ __forceinline__ void copy(int s) {
@@ -318,7 +331,7 @@ struct RowFeed {
 #pragma unroll
             for (int i = 0; i < 2 * NV; ++i) x[i] = make_float2(ahead[2 * i], ahead[2 * i + 1]);
             next += pitch;
-            if (--left > 0) bal_load<NV, VEC>(next, E, wt, lane, ahead);
+            if (--left > 0) bal_load<NV, VEC>(next, E, wt, lane, kBalPast, ahead);
         }
     }
     // Copies that were started and not used land before the CTA ends.
@@ -430,30 +443,30 @@ __global__ void __launch_bounds__((CL ? kBalGradWarps : kBalWarps) * 32, 1) bala
             pick += pick_step;
             if (valid && t >= lo) {
                 float2 loc = make_float2(0.0f, 0.0f);
+                float big = 0.0f;
 #pragma unroll
                 for (int i = 0; i < NE / 2; ++i) {
-                    float2 slope;
-                    x[i] = sigmoid2(x[i], slope);
+                    float2 e;
+                    x[i] = sigmoid2(x[i], e, big);
                     loc = add2(loc, x[i]);
                 }
-                float S = tm.sum(loc.x + loc.y);
-                float inv = rcp_approx(S);
-                if (S < kBalTinySum) {      // once more, relative to the row's largest
-                    float y[NE], m = -INFINITY, sum = 0.0f;
-                    bal_load<NV, VEC>(a.logits + static_cast<size_t>(t) * a.E, a.E, tm.wt, lane, y);
+                float S = tm.sum(fmaf(big, 0.0f, loc.x + loc.y));      // NaN where `big` is infinite
+                if (!(S >= kBalTinySum)) {
+                    float y[NE], m = -INFINITY, sum = 0.0f, slope;
+                    bal_load<NV, VEC>(a.logits + static_cast<size_t>(t) * a.E, a.E, tm.wt, lane, -INFINITY, y);
 #pragma unroll
                     for (int i = 0; i < NE; ++i) m = fmaxf(m, y[i]);
                     m = tm.max(m);
 #pragma unroll
                     for (int i = 0; i < NE; ++i) {
-                        y[i] = m == -INFINITY ? 0.0f : ex2_approx((y[i] - m) * kLog2e);
+                        y[i] = sigmoid_over(y[i], m, slope);
                         sum += y[i];
                     }
                     S = tm.sum(sum);
-                    inv = S == 0.0f ? 0.0f : rcp_approx(S);
 #pragma unroll
                     for (int i = 0; i < NE / 2; ++i) x[i] = make_float2(y[2 * i], y[2 * i + 1]);
                 }
+                const float inv = S == 0.0f ? 0.0f : rcp_approx(S);
 #pragma unroll
                 for (int i = 0; i < NE / 2; ++i) acc[i] = fma2(x[i], make_float2(inv, inv), acc[i]);
                 if (id >= 0 && id < a.E) atomicAdd(&hist[id], 1);
@@ -613,9 +626,10 @@ __device__ __forceinline__ float gate_pick_grad(int id, float xj, float dw) {
     const float u = ex2_approx(fabsf(xj) * -kLog2e), r = rcp_approx(1.0f + u);
     float s = id < 0 ? 0.0f : xj >= 0.0f ? r : u * r;
     float tot = warp_tree_sum(s);
-    if (tot < kBalTinySum) {      // relative to the largest, as the rows of the loss
+    if (!(tot >= kBalTinySum)) {      // relative to the largest, as the rows of the loss
         const float m = warp_max(id >= 0 ? xj : -INFINITY);
-        s = id < 0 || xj == -INFINITY ? 0.0f : ex2_approx((xj - m) * kLog2e);
+        float slope;
+        s = id < 0 ? 0.0f : sigmoid_over(xj, m, slope);
         tot = warp_tree_sum(s);
     }
     // divided: a token's only pick has the weight 1 and no gradient
@@ -756,31 +770,33 @@ __global__ void __launch_bounds__(kBalGradWarps * 32, 1) gate_grad_kernel(const 
         float2 S2 = make_float2(0.0f, 0.0f), G2 = S2;
         if (BAL && in_seq) {
             float2 sum = make_float2(0.0f, 0.0f), dot = sum;
-            float2 keep[NE / 2];
+            float big = 0.0f;
 #pragma unroll
             for (int i = 0; i < NE / 2; ++i) {
-                const float2 s = sigmoid2(x[i], keep[i]);
+                float2 e;
+                const float2 s = sigmoid2(x[i], e, big);
+                x[i] = mul2(mul2(e, s), s);         // s (1 - s) = exp(-x) s^2
                 sum = add2(sum, s);
                 dot = fma2(g[i], s, dot);
             }
-            float2 all = tm.sum(make_float2(sum.x + sum.y, dot.x + dot.y));
-            if (all.x < kBalTinySum) {
-                float m = -INFINITY;
+            float2 all = tm.sum(make_float2(fmaf(big, 0.0f, sum.x + sum.y), dot.x + dot.y));
+            if (!(all.x >= kBalTinySum)) {
+                float y[NE], m = -INFINITY;
+                bal_load<NV, VEC>(a.logits + static_cast<size_t>(t) * a.E, a.E, tm.wt, lane, -INFINITY, y);
 #pragma unroll
-                for (int i = 0; i < NE / 2; ++i) m = fmaxf(m, fmaxf(x[i].x, x[i].y));
+                for (int i = 0; i < NE; ++i) m = fmaxf(m, y[i]);
                 m = tm.max(m);
-                sum = dot = make_float2(0.0f, 0.0f);
+                all = make_float2(0.0f, 0.0f);
 #pragma unroll
-                for (int i = 0; i < NE / 2; ++i) {
-                    keep[i] = m == -INFINITY ? make_float2(0.0f, 0.0f)
-                                             : make_float2(ex2_approx((x[i].x - m) * kLog2e), ex2_approx((x[i].y - m) * kLog2e));
-                    sum = add2(sum, keep[i]);
-                    dot = fma2(g[i], keep[i], dot);
+                for (int i = 0; i < NE; ++i) {
+                    float slope;
+                    const float s = sigmoid_over(y[i], m, slope);
+                    all.x += s;
+                    all.y = fmaf(i % 2 ? g[i / 2].y : g[i / 2].x, s, all.y);
+                    (i % 2 ? x[i / 2].y : x[i / 2].x) = slope;
                 }
-                all = tm.sum(make_float2(sum.x + sum.y, dot.x + dot.y));
+                all = tm.sum(all);
             }
-#pragma unroll
-            for (int i = 0; i < NE / 2; ++i) x[i] = keep[i];
             const float S = all.x == 0.0f ? 0.0f : __frcp_rn(all.x);
             const float G = all.y * S;
             S2 = make_float2(S, S), G2 = make_float2(-G, -G);
@@ -793,17 +809,17 @@ __global__ void __launch_bounds__(kBalGradWarps * 32, 1) gate_grad_kernel(const 
         float* out = a.grad + static_cast<size_t>(t) * a.E;
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
-            const float2 lo = mul2(mul2(x[2 * v], S2), add2(g[2 * v], G2));
-            const float2 hi = mul2(mul2(x[2 * v + 1], S2), add2(g[2 * v + 1], G2));
+            const float2 lo = mul2(x[2 * v], S2), gl = add2(g[2 * v], G2);
+            const float2 hi = mul2(x[2 * v + 1], S2), gh = add2(g[2 * v + 1], G2);
             if constexpr (VEC) {
                 const int e = bal_expert<NV, VEC>(tm.wt, lane, 4 * v);
                 if (e < a.E) {
                     const float4 z = *reinterpret_cast<const float4*>(add + e);
-                    const float2 p = add2(lo, make_float2(z.x, z.y)), r = add2(hi, make_float2(z.z, z.w));
+                    const float2 p = fma2(lo, gl, make_float2(z.x, z.y)), r = fma2(hi, gh, make_float2(z.z, z.w));
                     __stcs(reinterpret_cast<float4*>(out + e), make_float4(p.x, p.y, r.x, r.y));
                 }
             } else {
-                const float w[4] = {lo.x, lo.y, hi.x, hi.y};
+                const float w[4] = {lo.x * gl.x, lo.y * gl.y, hi.x * gh.x, hi.y * gh.y};
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int e = bal_expert<NV, VEC>(tm.wt, lane, 4 * v + i);
