@@ -636,7 +636,8 @@ def lora_add(base: torch.Tensor, x: torch.Tensor, a: torch.Tensor, b: torch.Tens
 
     base and out are float32 or bfloat16, x [T, H], a [L, R, H] and b [L, N, R]
     bfloat16.  ``out=base`` works in place; without ``out`` a tensor is
-    allocated, and so is ``workspace`` (uint8, ``lora_workspace_size`` bytes)."""
+    allocated, and so is ``workspace`` (uint8, ``lora_workspace_size`` bytes, 0 up
+    to 256 tokens)."""
     fn = "lora_add"
     bf16 = base.dtype == torch.bfloat16
     _want(base, torch.bfloat16 if bf16 else torch.float32, "base")
@@ -658,10 +659,14 @@ def lora_add(base: torch.Tensor, x: torch.Tensor, a: torch.Tensor, b: torch.Tens
     if out.shape != base.shape:
         raise ValueError(f"{fn}: shape mismatch")
     if workspace is None:
-        workspace = torch.empty(lora_workspace_size(T, H, N, R, L), dtype=torch.uint8, device=base.device)
-    _want(workspace, torch.uint8, "workspace")
+        need = load().lora_workspace_size(T, H, N, R, L)
+        if need > 0:
+            workspace = torch.empty(need, dtype=torch.uint8, device=base.device)
+    else:
+        _want(workspace, torch.uint8, "workspace")
     _enqueue(fn, (base, x, a, b, adapter_ids, scales, out, workspace), stream, _at(base), int(bf16), _at(x), T, H,
-             _at(a), _at(b), N, R, L, _at(adapter_ids), _at(scales), _at(out), _at(workspace), workspace.numel())
+             _at(a), _at(b), N, R, L, _at(adapter_ids), _at(scales), _at(out), _at(workspace),
+             0 if workspace is None else workspace.numel())
     return out
 
 

@@ -371,10 +371,12 @@ int lora_add(const void* base, int base_bf16, const uint16_t* x, int T, int H, c
         overlap(out, nout, a, l * H) || overlap(out, nout, b, l * N))
         return fail(MB_ERR_INVALID_ARG, "%s: out overlaps an input (only out == base is allowed)", fn);
     const size_t need = lora_workspace_bytes(T, H, N, R, L);
-    if (!workspace || workspace_bytes < need)
-        return fail(MB_ERR_INVALID_ARG, "%s: needs a workspace of %zu bytes (got %zu)", fn, need,
-                    workspace ? workspace_bytes : static_cast<size_t>(0));
-    if (!aligned256(workspace)) return fail(MB_ERR_INVALID_ARG, "%s: workspace must be 256-byte aligned", fn);
+    if (need > 0) {
+        if (!workspace || workspace_bytes < need)
+            return fail(MB_ERR_INVALID_ARG, "%s: needs a workspace of %zu bytes (got %zu)", fn, need,
+                        workspace ? workspace_bytes : static_cast<size_t>(0));
+        if (!aligned256(workspace)) return fail(MB_ERR_INVALID_ARG, "%s: workspace must be 256-byte aligned", fn);
+    }
     const LoraLaunch ll{base, out, base_bf16 != 0, x, a, b, adapter_ids, scales, T, H, N, R, L, workspace};
     return cuda_status(launch_lora_add(ll, static_cast<cudaStream_t>(stream)), fn);
 }

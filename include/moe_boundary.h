@@ -356,8 +356,9 @@ int router_logits(const uint16_t* x, int T, int H, const uint16_t* w3, int E, fl
  *   a  [L, R, H] BF16       b  [L, N, R] BF16
  *   adapter_ids  [T] int32  scales  [L] FP32, or NULL for 1
  *   workspace  device scratch of lora_workspace_size(T, H, N, R, L) bytes,
- *              256-byte aligned; needs no initialisation; two calls that
- *              overlap on the GPU need two
+ *              256-byte aligned (may be NULL when that size is 0: T <= 256);
+ *              needs no initialisation; two calls that overlap on the GPU need
+ *              two
  * v and the sums over r are FP32 (products of BF16 values are exact in FP32),
  * out is rounded once.  No atomics: results are the same run to run.
  * Supported: H % 8 == 0, 8 <= H <= 65536, N % 8 == 0, 8 <= N <= 262144,

@@ -178,6 +178,7 @@ def test_refusals(cuda_dev):
         buf = torch.zeros(4 * 32 + 4, device=cuda_dev)
         call(base=buf[:128].view(4, 32), out=buf[4:].view(4, 32))
     with pytest.raises(eb.MoEBoundaryError, match="workspace"):
-        call(workspace=torch.empty(16, dtype=torch.uint8, device=cuda_dev))
+        eb.lora_add(**_inputs(cuda_dev, 300, 64, 32, 8, 2, False),
+                    workspace=torch.empty(16, dtype=torch.uint8, device=cuda_dev))
     with pytest.raises(eb.MoEBoundaryError, match="needs H, N and R"):
         call(a=i["a"][:, :4].contiguous(), b=i["b"][:, :, :4].contiguous())

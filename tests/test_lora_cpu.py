@@ -38,9 +38,10 @@ def test_library_refuses_before_any_launch():
         assert call(**{name: N0}) == 1 and "null" in eb.last_error()
         assert call(**{name: odd}) == 1 and "aligned" in eb.last_error()
     assert call(scales=odd) == 1
-    assert call(ws=N0) == 1 and "workspace" in eb.last_error()
-    need = eb.lora_workspace_size(4, 64, 32, 8, 2)
-    assert need > 0 and call(size=need - 1) == 1 and call(ws=odd) == 1
+    assert eb.lora_workspace_size(4, 64, 32, 8, 2) == 0       # few tokens need none
+    assert call(T=300, ws=N0) == 1 and "workspace" in eb.last_error()
+    need = eb.lora_workspace_size(300, 64, 32, 8, 2)
+    assert need > 0 and call(T=300, size=need - 1) == 1 and call(T=300, ws=odd) == 1
     # out is base itself or apart from every input
     shifted = ctypes.c_void_p((1 << 32) + 16)
     assert call(out=shifted) == 1 and "overlaps" in eb.last_error()
