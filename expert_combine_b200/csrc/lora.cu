@@ -470,6 +470,15 @@ struct Ring {
     }
 };
 
+// A warp's wait: one lane polls (a CTA of polling warps takes the issue slots of
+// the one thread that feeds the tensor core: 50 against 47 us at 8192 x 8192).
+__device__ __forceinline__ bool lm_wait_warp(uint64_t* bar, int parity) {
+    int ok = 1;
+    if ((threadIdx.x & 31) == 0) ok = mbar_wait_bounded(bar, static_cast<uint32_t>(parity), kLmTimeout) ? 1 : 0;
+    __syncwarp();
+    return __shfl_sync(0xffffffffu, ok, 0) != 0;
+}
+
 // Waits (bounded) until the last copy issued into each slot of a ring has landed.
 __device__ __forceinline__ void lm_drain(uint64_t* full, int n, int issued) {
     for (int j = issued > n ? issued - n : 0; j < issued; ++j)
@@ -508,8 +517,7 @@ __global__ void __launch_bounds__(kLmThreads, 1) lora_shrink_kernel(const __grid
     extern __shared__ uint8_t lm_raw[];
     const uint32_t raw = smem_addr(lm_raw);
     uint8_t* ring = lm_raw + (((raw + 1023u) & ~1023u) - raw);
-    __shared__ __align__(8) uint64_t x_full[kLmMaxStages], a_full[kLmMaxStages], empty[kLmMaxStages], acc_full[2],
-        acc_empty[2], done;
+    __shared__ __align__(8) uint64_t full[kLmMaxStages], empty[kLmMaxStages], acc_full[2], acc_empty[2], done;
     __shared__ uint32_t s_tmem;
     __shared__ int s_issued, s_last;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -517,8 +525,7 @@ __global__ void __launch_bounds__(kLmThreads, 1) lora_shrink_kernel(const __grid
     const uint32_t cols = a.rn <= 16 ? 32u : a.rn <= 32 ? 64u : a.rn <= 64 ? 128u : 256u;   // two accumulators
     if (threadIdx.x == 0) {
         for (int i = 0; i < S; ++i) {
-            mbar_init(&x_full[i], 128);
-            mbar_init(&a_full[i], 1);
+            mbar_init(&full[i], 128 + 1);        // the loading threads' rows and the TMA's A
             mbar_init(&empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -556,11 +563,11 @@ __global__ void __launch_bounds__(kLmThreads, 1) lora_shrink_kernel(const __grid
                     arow = a.tiles[++tile].adapter * a.R;
                 }
                 if (issued >= S && !mbar_wait_bounded(&empty[r.slot], static_cast<uint32_t>(r.phase ^ 1), kLmTimeout)) break;
-                mbar_arrive_expect_tx(&a_full[r.slot], static_cast<uint32_t>(kLmStep * a_bytes));
+                mbar_arrive_expect_tx(&full[r.slot], static_cast<uint32_t>(kLmStep * a_bytes));
 #pragma unroll
                 for (int h = 0; h < kLmStep; ++h)
                     tma_load_2d(smem_addr(ring) + r.slot * stage_bytes + kLmStep * kLmSlabBytes + h * a_bytes, &amap,
-                                (j * kLmStep + h) * kLmSlab, arow, &a_full[r.slot]);
+                                (j * kLmStep + h) * kLmSlab, arow, &full[r.slot]);
                 ++issued;
                 r.next(S);
             }
@@ -577,14 +584,13 @@ __global__ void __launch_bounds__(kLmThreads, 1) lora_shrink_kernel(const __grid
             const int j0 = static_cast<int>(u % J), j1 = static_cast<int>(min(static_cast<int64_t>(J), j0 + (u1 - u)));
             rows.tile(a, a.tiles[u / J]);
             for (int j = j0; j < j1; ++j) {
-                ok = issued < S || mbar_wait_bounded(&empty[r.slot], static_cast<uint32_t>(r.phase ^ 1), kLmTimeout);
-                ok = __all_sync(0xffffffffu, ok);
+                ok = issued < S || lm_wait_warp(&empty[r.slot], r.phase ^ 1);
                 if (!ok) break;
 #pragma unroll
                 for (int h = 0; h < kLmStep; ++h)
                     rows.load(smem_addr(ring) + r.slot * stage_bytes + h * kLmSlabBytes, a.x, pitch,
                               static_cast<size_t>(j * kLmStep + h) * 128);
-                cp_async_arrive(&x_full[r.slot]);
+                cp_async_arrive(&full[r.slot]);
                 ++issued;
                 r.next(S);
             }
@@ -595,6 +601,8 @@ __global__ void __launch_bounds__(kLmThreads, 1) lora_shrink_kernel(const __grid
         if (lane == 0) {
             Ring r;
             const uint32_t idesc = lm_idesc(a.rn);
+            const uint64_t x_desc = smem_desc_sw128(smem_addr(ring)),
+                           a_desc = smem_desc_sw128(smem_addr(ring) + kLmStep * kLmSlabBytes);
             bool ok = true;
             int seg = 0;
             for (int64_t u = u0; ok && u < u1; ++seg) {
@@ -604,21 +612,22 @@ __global__ void __launch_bounds__(kLmThreads, 1) lora_shrink_kernel(const __grid
                 if (seg >= 2 && !mbar_wait_bounded(&acc_empty[b], static_cast<uint32_t>(((seg >> 1) - 1) & 1), kLmTimeout))
                     break;
                 tc_fence_after();
+                const uint32_t acc = tmem + b * (cols / 2);
                 for (int j = j0; j < j1; ++j) {
-                    ok = mbar_wait_bounded(&a_full[r.slot], static_cast<uint32_t>(r.phase), kLmTimeout) &&
-                         mbar_wait_bounded(&x_full[r.slot], static_cast<uint32_t>(r.phase), kLmTimeout);
+                    ok = mbar_wait_bounded(&full[r.slot], static_cast<uint32_t>(r.phase), kLmTimeout);
                     if (!ok) break;
                     // the rows were written through the generic proxy, by copies that the barrier has seen land;
                     // the MMA reads through the async proxy
                     fence_proxy_async_smem();
                     tc_fence_after();
-                    const uint32_t sx = smem_addr(ring) + r.slot * stage_bytes, sa = sx + kLmStep * kLmSlabBytes;
+                    // descriptors count in 16 bytes; what a step adds stays inside their address field
+                    const uint64_t dx = x_desc + static_cast<uint32_t>(r.slot * stage_bytes >> 4),
+                                   da = a_desc + static_cast<uint32_t>(r.slot * stage_bytes >> 4);
 #pragma unroll
                     for (int h = 0; h < kLmStep; ++h)
 #pragma unroll
                         for (int k = 0; k < kLmSlab / 16; ++k)
-                            mma_bf16(tmem + b * (cols / 2), smem_desc_sw128(sx + h * kLmSlabBytes + 32u * k),
-                                     smem_desc_sw128(sa + h * a_bytes + 32u * k), idesc,
+                            mma_bf16(acc, dx + (h * kLmSlabBytes + 32 * k >> 4), da + (h * a_bytes + 32 * k >> 4), idesc,
                                      (j != j0 || h != 0 || k != 0) ? 1u : 0u);
                     mma_commit(&empty[r.slot]);
                     r.next(S);
@@ -652,7 +661,7 @@ __global__ void __launch_bounds__(kLmThreads, 1) lora_shrink_kernel(const __grid
             bool ok = true;
             for (int j = j0; j < j1; j += kLmChain, ++seg) {
                 const int b = seg & 1;
-                ok = mbar_wait_bounded(&acc_full[b], static_cast<uint32_t>((seg >> 1) & 1), kLmTimeout) && ok;
+                ok = lm_wait_warp(&acc_full[b], (seg >> 1) & 1) && ok;
                 tc_fence_after();
                 const uint32_t acc = tmem + b * (cols / 2) + (static_cast<uint32_t>(32 * quad) << 16);
 #pragma unroll
@@ -716,9 +725,9 @@ __global__ void __launch_bounds__(kLmThreads, 1) lora_shrink_kernel(const __grid
             u += j1 - j0;       // s_last is set again only behind the next tile's first barrier
         }
     }
-    mbar_wait_bounded(&done, 0u, kLmTimeout);
+    if (threadIdx.x == 0) mbar_wait_bounded(&done, 0u, kLmTimeout);
     __syncthreads();
-    if (threadIdx.x == 0) lm_drain(a_full, S, s_issued);
+    if (threadIdx.x == 0) lm_drain(full, S, s_issued);
     tc_fence_after();
     __syncthreads();
     if (warp == 0) tmem_dealloc(tmem, cols);
@@ -827,9 +836,7 @@ __global__ void __launch_bounds__(kLmThreads, 1) lora_expand_kernel(const __grid
                 rows.tile(a, a.tiles[tile]);
             }
             for (int s = 0; s < kSubs && n0 + s * kSubCols < a.N; ++s) {
-                ok = nx < a.base_stages ||
-                     mbar_wait_bounded(&base_empty[rx.slot], static_cast<uint32_t>(rx.phase ^ 1), kLmTimeout);
-                ok = __all_sync(0xffffffffu, ok);
+                ok = nx < a.base_stages || lm_wait_warp(&base_empty[rx.slot], rx.phase ^ 1);
                 if (!ok) break;
                 rows.load(smem_addr(sbase) + rx.slot * kLmSlabBytes, a.base, pitch,
                           static_cast<size_t>(n0 + s * kSubCols) * sizeof(O));
@@ -922,13 +929,12 @@ __global__ void __launch_bounds__(kLmThreads, 1) lora_expand_kernel(const __grid
                     token[it] = r < count ? a.row_token[t.row0 + r] : 0;
                 }
             }
-            bool ok = mbar_wait_bounded(&acc_full[b], static_cast<uint32_t>((i >> 1) & 1), kLmTimeout);
+            bool ok = lm_wait_warp(&acc_full[b], (i >> 1) & 1);
             tc_fence_after();
             const uint32_t acc = tmem + b * kLmCols + (static_cast<uint32_t>(32 * quad) << 16);
             for (int s = 0; s < kSubs && n0 + s * kSubCols < a.N; ++s, rx.next(a.base_stages)) {
                 if ((s & 1) != grp) continue;
-                ok = mbar_wait_bounded(&base_full[rx.slot], static_cast<uint32_t>(rx.phase), kLmTimeout) && ok;
-                ok = __all_sync(0xffffffffu, ok);
+                ok = lm_wait_warp(&base_full[rx.slot], rx.phase) && ok;
                 if (!ok) break;
                 const uint32_t tile_s = smem_addr(sbase) + rx.slot * kLmSlabBytes;
                 const uint32_t mine = tile_s + row * 128;
@@ -973,13 +979,13 @@ __global__ void __launch_bounds__(kLmThreads, 1) lora_expand_kernel(const __grid
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&base_empty[rx.slot]);
             }
-            if (!__all_sync(0xffffffffu, ok)) break;
+            if (!ok) break;
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&acc_empty[b]);
         }
     }
-    mbar_wait_bounded(&done, 0u, kLmTimeout);
+    if (threadIdx.x == 0) mbar_wait_bounded(&done, 0u, kLmTimeout);
     __syncthreads();
     if (threadIdx.x == 0) {
         lm_drain(v_full, a.v_bufs, s_issued[0]);
