@@ -350,12 +350,19 @@ __global__ void __launch_bounds__(1024) lora_tiles_kernel(const LmArgs a) {
 // (so the rows' order, and with it every sum's, is the same run to run) and the
 // tiles.  Warp w takes the w-th run of tokens 32 at a time; the lanes of one
 // adapter find each other by a match, and the warp's running count of that
-// adapter gives their places.  8192 tokens: 4 us, against 12 us for the
-// general dispatch and the tiles kernel, which take the larger batches.
+// adapter gives a token's place among the warp's tokens of the adapter.  The
+// general dispatch and the tiles kernel take the larger batches.
+__host__ __device__ __forceinline__ size_t lm_plan_bytes(int T, int L) {
+    return static_cast<size_t>(2 * ((T + 7) / 8 * 8) + (32 * L + 7) / 8 * 8) * 2 + static_cast<size_t>(2 * (L + 1)) * 4;
+}
+
 __global__ void __launch_bounds__(1024) lora_plan_kernel(const LmArgs a) {
     extern __shared__ __align__(16) uint8_t plan_raw[];
     uint16_t* sid = reinterpret_cast<uint16_t*>(plan_raw);      // [T] adapter, 0xffff: none
-    uint16_t* cnt = sid + (a.T + 7) / 8 * 8;                    // [32][L]
+    uint16_t* place = sid + (a.T + 7) / 8 * 8;                  // [T] among the warp's tokens of the adapter
+    uint16_t* cnt = place + (a.T + 7) / 8 * 8;                  // [32][L] the warps' counts, then their first rows
+    int* first_row = reinterpret_cast<int*>(cnt + (32 * a.L + 7) / 8 * 8);   // [L + 1]
+    int* first_tile = first_row + a.L + 1;                                   // [L + 1]
     __shared__ int2 s_warp[32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     for (int i = tid; i < 32 * a.L; i += 1024) cnt[i] = 0;
@@ -370,55 +377,74 @@ __global__ void __launch_bounds__(1024) lora_plan_kernel(const LmArgs a) {
     const int span = (a.T + 1023) / 1024 * 32, lo = warp * span, hi = min(a.T, lo + span);
     uint16_t* mine = cnt + warp * a.L;
     for (int i0 = lo; i0 < hi; i0 += 32) {
-        const int e = i0 + lane < hi ? sid[i0 + lane] : 0xffff;
-        const uint32_t m = __match_any_sync(0xffffffffu, e);
-        if (e != 0xffff && (m & ((1u << lane) - 1u)) == 0) mine[e] = static_cast<uint16_t>(mine[e] + __popc(m));
-        __syncwarp();
-    }
-    __syncthreads();
-    int c[32], total = 0;       // the warps' counts of adapter `tid`
-#pragma unroll
-    for (int w = 0; w < 32; ++w) c[w] = tid < a.L ? cnt[w * a.L + tid] : 0;
-#pragma unroll
-    for (int w = 0; w < 32; ++w) total += c[w];
-    const int tiles = (total + kLmTile - 1) / kLmTile;
-    int2 scan = make_int2(total, tiles);
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-        const int p = __shfl_up_sync(0xffffffffu, scan.x, off), q = __shfl_up_sync(0xffffffffu, scan.y, off);
-        if (lane >= off) scan.x += p, scan.y += q;
-    }
-    if (lane == 31) s_warp[warp] = scan;
-    __syncthreads();
-    int row = scan.x - total, tile = scan.y - tiles, all = 0;
-    for (int w = 0; w < 32; ++w) {
-        if (w < warp) row += s_warp[w].x, tile += s_warp[w].y;
-        all += s_warp[w].y;
-    }
-    if (tid < a.L) {
-        for (int i = 0; i < tiles; ++i)
-            a.tiles[tile + i] = LmTile{tid, row + i * kLmTile, min(kLmTile, total - i * kLmTile), 0};
-        int at = row;
-#pragma unroll
-        for (int w = 0; w < 32; ++w) {
-            cnt[w * a.L + tid] = static_cast<uint16_t>(at);     // first row of this warp's tokens of the adapter
-            at += c[w];
-        }
-    }
-    if (tid == 0) *a.ntiles = all;
-    for (int i = tid; i < all; i += 1024) a.arrived[i] = 0;
-    __syncthreads();
-    for (int i0 = lo; i0 < hi; i0 += 32) {
-        const int e = i0 + lane < hi ? sid[i0 + lane] : 0xffff;
-        const uint32_t m = __match_any_sync(0xffffffffu, e);
-        const uint32_t below = m & ((1u << lane) - 1u);
-        const int first = e != 0xffff ? mine[e] : 0;
+        const int i = i0 + lane, e = i < hi ? sid[i] : 0xffff;
+        const uint32_t same = __match_any_sync(0xffffffffu, e), below = same & ((1u << lane) - 1u);
+        const int before = e != 0xffff ? mine[e] : 0;
         __syncwarp();
         if (e != 0xffff) {
-            a.row_token[first + __popc(below)] = i0 + lane;
-            if (below == 0) mine[e] = static_cast<uint16_t>(first + __popc(m));
+            place[i] = static_cast<uint16_t>(before + __popc(below));
+            if (below == 0) mine[e] = static_cast<uint16_t>(before + __popc(same));
         }
         __syncwarp();
+    }
+    __syncthreads();
+    // rows and tiles of adapter `tid`, summed over the warps, then over the adapters before it
+    const bool some = warp * 32 < a.L;          // this warp has an adapter
+    int c[32];
+    int2 own = make_int2(0, 0), scan;
+    if (some) {
+#pragma unroll
+        for (int w = 0; w < 32; ++w) c[w] = tid < a.L ? cnt[w * a.L + tid] : 0;
+#pragma unroll
+        for (int w = 0; w < 32; ++w) own.x += c[w];
+        own.y = (own.x + kLmTile - 1) / kLmTile;
+        scan = own;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int p = __shfl_up_sync(0xffffffffu, scan.x, off), q = __shfl_up_sync(0xffffffffu, scan.y, off);
+            if (lane >= off) scan.x += p, scan.y += q;
+        }
+    }
+    if (lane == 31) s_warp[warp] = some ? scan : make_int2(0, 0);
+    __syncthreads();
+    if (some) {
+        int2 before = make_int2(0, 0);
+        for (int w = 0; w < warp; ++w) before.x += s_warp[w].x, before.y += s_warp[w].y;
+        if (tid < a.L) {
+            int at = before.x + scan.x - own.x;
+            first_row[tid] = at;
+            first_tile[tid] = before.y + scan.y - own.y;
+            if (tid == a.L - 1) {
+                first_row[a.L] = at + own.x;
+                first_tile[a.L] = before.y + scan.y;
+            }
+#pragma unroll
+            for (int w = 0; w < 32; ++w) {
+                cnt[w * a.L + tid] = static_cast<uint16_t>(at);
+                at += c[w];
+            }
+        }
+    }
+    __syncthreads();
+#pragma unroll 8
+    for (int i = lo + lane; i < hi; i += 32) {
+        const int e = sid[i];
+        if (e != 0xffff) a.row_token[mine[e] + place[i]] = i;
+    }
+    const int all = first_tile[a.L];
+    if (tid == 0) *a.ntiles = all;
+    for (int i = tid; i < all; i += 1024) {
+        int e = 0, behind = a.L;                // the adapter whose tiles hold i
+        while (behind - e > 1) {
+            const int mid = (e + behind) >> 1;
+            if (first_tile[mid] <= i)
+                e = mid;
+            else
+                behind = mid;
+        }
+        const int row0 = first_row[e] + (i - first_tile[e]) * kLmTile;
+        a.tiles[i] = LmTile{e, row0, min(kLmTile, first_row[e + 1] - row0), 0};
+        a.arrived[i] = 0;
     }
 }
 
@@ -1082,9 +1108,9 @@ cudaError_t launch_lora_many(const LoraLaunch& l, cudaStream_t s) {
     void* targs[] = {&a};
     if (lm_one_plan(l.T, l.L)) {
         const void* plan = reinterpret_cast<const void*>(lora_plan_kernel);
-        const size_t psmem = static_cast<size_t>((l.T + 7) / 8 * 8 + 32 * l.L) * 2;
+        const size_t psmem = lm_plan_bytes(l.T, l.L);
         e = cudaFuncSetAttribute(plan, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 (kLmPlanTokens + 32 * kLmPlanAdapters) * 2);
+                                 static_cast<int>(lm_plan_bytes(kLmPlanTokens, kLmPlanAdapters)));
         if (e == cudaSuccess) e = lm_launch(plan, 1, 1024, psmem, targs, s);
     } else {
         e = launch_dispatch(l.ids, l.T, 1, 0, l.L, offsets, row_idx, row_token, w + at.dispatch, s);

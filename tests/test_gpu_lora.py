@@ -68,7 +68,8 @@ def _check(i, out=None):
                                        (17, 1032, 40, 16, 3), (33, 2048, 512, 32, 40), (100, 4104, 1000, 40, 7),
                                        (128, 1024, 2048, 128, 16), (255, 512, 128, 64, 5), (256, 512, 72, 96, 4),
                                        (257, 520, 136, 16, 6), (300, 1024, 256, 64, 1), (777, 1536, 520, 48, 9),
-                                       (1500, 2048, 2560, 16, 4), (2300, 264, 24, 128, 64)])
+                                       (1500, 2048, 2560, 16, 4), (2300, 264, 24, 128, 64),
+                                       (300, 64, 16, 8, 1100), (33000, 72, 16, 8, 3), (4500, 64, 24, 16, 1025)])
 def test_sizes(cuda_dev, T, H, N, R, L, bf16):
     _check(_inputs(cuda_dev, T, H, N, R, L, bf16, seed=T + H))
 
