@@ -44,6 +44,10 @@ constexpr int kBalLane = 16;                 // most logits per lane
 constexpr int kBalMaxTeam = kMaxExperts / (32 * kBalLane);
 constexpr int kBalWarps = 24;                // most warps of a CTA (one CTA per SM): the loss
 constexpr int kBalGradWarps = 16;            // of the gradient, which needs twice the registers, and of a cluster's CTAs
+constexpr int kBalGateWarps = 4;             // warps of the gradient for the gate's own part
+static_assert(kBalGradWarps <= 4 * kBalGateWarps, "a gate warp serves four teams at most");
+constexpr int kBalTags = 1024;               // marks per row for finding repeated picks
+constexpr int kBalLists = 4;                 // lists of entries a team has under way
 constexpr int kBalRowsPerTeam = 128;         // most rows a team adds up in one FP32 register
 constexpr int kBalTargetCtas = 148;
 constexpr int kBalRing = 8;                  // most row slots of a warp
@@ -69,6 +73,9 @@ struct BalPlan {
     bool cluster; // forward pass in one cluster
 };
 
+// Lanes per row of picks.
+__host__ __device__ __forceinline__ int bal_group(int k) { return k <= 8 ? 8 : k <= 16 ? 16 : 32; }
+
 BalPlan bal_plan(int T, int E, int Q, bool grad) {
     BalPlan p;
     p.W = (E + 32 * kBalLane - 1) / (32 * kBalLane);
@@ -87,7 +94,7 @@ BalPlan bal_plan(int T, int E, int Q, bool grad) {
     p.ctas = T == 0 ? 1 : static_cast<int>((static_cast<int64_t>(T) + p.tokens - 1) / p.tokens);
     p.ring = 0;
     if (E % 4 == 0) {
-        p.ring = (p.W == 1 ? kBalRingBytes : kBalRingBytes * 3 / 4) / (p.W * p.teams * p.nv * 512);
+        p.ring = kBalRingBytes / (p.W * p.teams * p.nv * 512);
         if (p.ring > kBalRing) p.ring = kBalRing;
         if (p.ring > rows) p.ring = static_cast<int>(rows);
     }
@@ -208,12 +215,6 @@ struct Team {
     }
     __device__ __forceinline__ float sum(float v) { return join<false>(make_float2(warp_tree_sum(v), 0.0f)).x; }
     __device__ __forceinline__ float max(float v) { return join<true>(make_float2(warp_max(v), 0.0f)).x; }
-    __device__ __forceinline__ void sync() {
-        if (W == 1)
-            __syncwarp();
-        else
-            named_bar_sync(bar, W * 32);
-    }
     template <bool MAX>
     __device__ __forceinline__ float2 join(float2 v) {
         if (W == 1) {
@@ -620,70 +621,202 @@ __global__ void __launch_bounds__(kFinExperts * kFinLanes) balance_finish_kernel
     }
 }
 
-// What a row's picks get from the gate's own gradient: lane j's pick `id` (-1:
-// none) with logit xj and incoming gradient dw.
-__device__ __forceinline__ float gate_pick_grad(int id, float xj, float dw) {
-    const float u = ex2_approx(fabsf(xj) * -kLog2e), r = rcp_approx(1.0f + u);
-    float s = id < 0 ? 0.0f : xj >= 0.0f ? r : u * r;
-    float tot = warp_tree_sum(s);
-    if (!(tot >= kBalTinySum)) {      // relative to the largest, as the rows of the loss
-        const float m = warp_max(id >= 0 ? xj : -INFINITY);
-        float slope;
-        s = id < 0 ? 0.0f : sigmoid_over(xj, m, slope);
-        tot = warp_tree_sum(s);
-    }
-    // divided: a token's only pick has the weight 1 and no gradient
-    const float w = tot == 0.0f ? 0.0f : __fdiv_rn(s, tot);
-    const float dot = warp_tree_sum(dw * w);
-    float d = w * (xj >= 0.0f ? u * r : r) * (dw - dot);
-    const unsigned same = __match_any_sync(0xffffffffu, id);
-    if (__any_sync(0xffffffffu, id >= 0 && __popc(same) > 1)) {   // the same expert twice: added in slot order
-        float z = 0.0f;
-        for (int j = 0; j < 32; ++j) {
-            const float dj = __shfl_sync(0xffffffffu, d, j);
-            if (same >> j & 1u) z += dj;
+template <bool MAX, int M>
+__device__ __forceinline__ void group_join(float (&v)[M], int G) {      // each over the G lanes of a row
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        if (off >= 8 && off >= G) break;      // G is 8, 16 or 32
+#pragma unroll
+        for (int j = 0; j < M; ++j) {
+            const float o = __shfl_xor_sync(0xffffffffu, v[j], off);
+            v[j] = MAX ? fmaxf(v[j], o) : v[j] + o;
         }
-        d = z;
     }
-    return d;
 }
 
-// The gradient of the logits.  A team keeps its row in registers; the few
-// entries of the gate's own gradient are laid into a row of shared memory
-// (zero elsewhere) that the dense pass adds, so every logit's gradient is
-// written once, in full lines.  In a team of several warps they take turns at
-// the gate: warp i % W forms row i's entries while the others are a row behind
-// (three such rows in turn: being cleared, read and filled); a warp alone needs
-// one.  Picks are fetched two turns ahead, their logits and gradients one.
+// The gate's own gradient for M times the picks of 32 / G rows, G lanes a
+// row (G a power of two >= k): this lane's picks `id` (-1: none) with logits xj
+// and incoming gradients dw.  The rows are independent, so their chains of sums
+// run side by side.  `tags`: two times kBalTags bytes a row of the warp's own
+// shared memory, any contents.
+template <int M>
+__device__ __forceinline__ void gate_pick_grad(const int (&id)[M], const float (&xj)[M],
+                                               const float (&dw)[M], int G, volatile uint8_t* tags,
+                                               float (&d)[M]) {
+    const int lane = threadIdx.x & 31;
+    float s[M], om[M], tot[M];
+    int tiny = 0, twice = 0;
+#pragma unroll
+    for (int j = 0; j < M; ++j) {
+        // Two picks of one expert find each other's mark; so may two of 1024 experts apart, which the match below
+        // tells from them (a match costs about 1000 cycles for 32 different values).  The marks alternate between
+        // two areas, so one is written while the other may still be read.
+        volatile uint8_t* tag = tags + (((j & 1) * 32 + lane) / G * kBalTags) + (id[j] & (kBalTags - 1));
+        if (id[j] >= 0) *tag = static_cast<uint8_t>(lane);
+        __syncwarp();
+        twice |= id[j] >= 0 ? *tag ^ lane : 0;
+    }
+#pragma unroll
+    for (int j = 0; j < M; ++j) {
+        const float u = ex2_approx(fabsf(xj[j]) * -kLog2e), r = rcp_approx(1.0f + u);
+        om[j] = xj[j] >= 0.0f ? u * r : r;
+        s[j] = id[j] < 0 ? 0.0f : xj[j] >= 0.0f ? r : u * r;
+        tot[j] = s[j];
+    }
+    group_join<false, M>(tot, G);
+#pragma unroll
+    for (int j = 0; j < M; ++j) tiny |= id[j] >= 0 && !(tot[j] >= kBalTinySum) ? 1 : 0;
+    if (__any_sync(0xffffffffu, tiny != 0)) {      // relative to the row's largest, as in the loss
+        float m[M], slope;
+#pragma unroll
+        for (int j = 0; j < M; ++j) m[j] = id[j] >= 0 ? xj[j] : -INFINITY;
+        group_join<true, M>(m, G);
+#pragma unroll
+        for (int j = 0; j < M; ++j) {
+            s[j] = id[j] < 0 ? 0.0f : sigmoid_over(xj[j], m[j], slope);
+            tot[j] = s[j];
+        }
+        group_join<false, M>(tot, G);
+    }
+    float dot[M];
+#pragma unroll
+    for (int j = 0; j < M; ++j) {
+        // divided: a token's only pick has the weight 1 and no gradient
+        s[j] = tot[j] == 0.0f ? 0.0f : __fdiv_rn(s[j], tot[j]);
+        dot[j] = id[j] < 0 ? 0.0f : dw[j] * s[j];
+    }
+    group_join<false, M>(dot, G);
+#pragma unroll
+    for (int j = 0; j < M; ++j) d[j] = s[j] * om[j] * (dw[j] - dot[j]);
+    if (__any_sync(0xffffffffu, twice != 0)) {   // the same expert twice in a row: added in slot order
+#pragma unroll
+        for (int j = 0; j < M; ++j) {
+            const unsigned same = __match_any_sync(0xffffffffu, id[j] < 0 ? -1 - lane : id[j] | (lane / G) << 16);
+            float z = 0.0f;
+#pragma unroll 1
+            for (int i = 0; i < 32; ++i) {
+                const float di = __shfl_sync(0xffffffffu, d[j], i);
+                if (same >> i & 1u) z += di;
+            }
+            d[j] = z;
+        }
+    }
+}
+
+// A gate warp's whole work: the lists of teams g, g + kBalGateWarps, ... (M of
+// them at most), side by side.  All loads go to valid places whether their values
+// count or not, and are looked at a turn later, so none is branched around or
+// waited for where it starts.
+template <int M>
+__device__ __forceinline__ void gate_lists(const BalArgs& a, int g, int t0, int t1, volatile uint8_t* tags,
+                                        int2 (*list)[kBalLists][32], uint64_t (*list_full)[kBalLists],
+                                        uint64_t (*list_empty)[kBalLists]) {
+    const int lane = threadIdx.x & 31;
+    const int G = bal_group(a.k), batch = 32 / G;
+    int lists[M];            // of each team
+#pragma unroll
+    for (int j = 0; j < M; ++j) {
+        const int team = g + j * kBalGateWarps;
+        const int rows = team < a.teams && t0 + team < t1 ? (t1 - t0 - team + a.teams - 1) / a.teams : 0;
+        lists[j] = (rows + batch - 1) / batch;
+    }
+    if (lists[0] == 0) return;
+    // this lane's token of list b and team g is first + b * step, those of the other teams kBalGateWarps further each
+    const int64_t first = t0 + g + static_cast<int64_t>(lane / G) * a.teams, step = static_cast<int64_t>(batch) * a.teams;
+    const int pick = min(lane % G, a.k - 1);
+    const uint32_t experts = lane % G < a.k ? static_cast<uint32_t>(a.E) : 0u;
+    int64_t tp = first, tv = first;         // token of the next fetch of picks and of values
+    auto fetch_picks = [&](int (&d)[M], int (&m)[M]) {
+#pragma unroll
+        for (int j = 0; j < M; ++j) {
+            const int64_t t = min(tp + j * kBalGateWarps, static_cast<int64_t>(t1 - 1));
+            d[j] = a.ids[t * a.k + pick];
+            m[j] = a.mask[t];
+        }
+        tp += step;
+    };
+    auto fetch_values = [&](int (&d)[M], const int (&m)[M], float (&x)[M], float (&w)[M]) {
+#pragma unroll
+        for (int j = 0; j < M; ++j) {
+            const int64_t t = min(tv + j * kBalGateWarps, static_cast<int64_t>(t1 - 1));
+            uint32_t below = tv + j * kBalGateWarps < t1 ? experts : 0u;      // ids that count are below it
+            below = m[j] != 0 ? below : 0u;
+            d[j] = static_cast<uint32_t>(d[j]) < below ? d[j] : -1;
+            x[j] = a.logits[t * a.E + max(d[j], 0)];
+            w[j] = a.grad_w[t * a.k + pick];
+        }
+        tv += step;
+    };
+    int id[M], id1[M], m1[M];
+    float xj[M], dw[M];
+    fetch_picks(id, m1);
+    fetch_values(id, m1, xj, dw);
+    fetch_picks(id1, m1);
+    int my_team = g, my_lists = 0;          // lanes 0 .. M - 1 see to a team each
+#pragma unroll
+    for (int j = 0; j < M; ++j)
+        if (lane == j) my_team = g + j * kBalGateWarps, my_lists = lists[j];
+    bool dead = false;
+    int slot = 0, phase = 1;
+    for (int b = 0; b < lists[0]; ++b) {
+        int id2[M], m2[M];
+        float xj1[M], dw1[M], d[M];
+        fetch_picks(id2, m2);
+        fetch_values(id1, m1, xj1, dw1);
+        gate_pick_grad(id, xj, dw, G, tags, d);
+        if (b >= kBalLists && b < my_lists && !dead)      // a team takes every list that is made for it
+            dead = !mbar_wait_bounded(&list_empty[my_team][slot], static_cast<uint32_t>(phase), kBalTimeout);
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < M; ++j)
+            if (b < lists[j]) list[g + j * kBalGateWarps][slot][lane] = make_int2(id[j], __float_as_int(d[j]));
+        __syncwarp();
+        if (b < my_lists) mbar_arrive(&list_full[my_team][slot]);
+        if (++slot == kBalLists) slot = 0, phase ^= 1;
+#pragma unroll
+        for (int j = 0; j < M; ++j)
+            id[j] = id1[j], id1[j] = id2[j], m1[j] = m2[j], xj[j] = xj1[j], dw[j] = dw1[j];
+    }
+}
+
+// The gradient of the logits.  A team of warps keeps its row in registers, as in
+// the loss.  The gate's own gradient, a chain of dependent sums over few lanes,
+// is the work of kBalGateWarps warps beside the teams: each serves every
+// kBalGateWarps-th team and leaves the entries (expert, gradient) of 32 / G rows
+// at a time in the team's ring of lists.  A warp of the team lays the entries
+// that fall to its part of the row into a part-row of shared memory (zero
+// elsewhere) and adds that in the dense pass, so every logit's gradient is
+// written once, in full lines.  (With the gate in the teams themselves 32768 x
+// 2560 took 177 us instead of 131.)
 template <int NV, bool VEC, bool BAL>
-__global__ void __launch_bounds__(kBalGradWarps * 32, 1) gate_grad_kernel(const BalArgs a) {
+__global__ void __launch_bounds__((kBalGradWarps + kBalGateWarps) * 32, 1) gate_grad_kernel(const BalArgs a) {
     constexpr int NE = 4 * NV;
     extern __shared__ __align__(128) uint8_t bal_smem[];
     __shared__ float2 red[kBalGradWarps][2 * kBalMaxTeam];
     __shared__ __align__(8) uint64_t bars[kBalGradWarps * kBalRing];
+    __shared__ __align__(8) uint64_t list_full[kBalGradWarps][kBalLists], list_empty[kBalGradWarps][kBalLists];
+    __shared__ int2 list[kBalGradWarps][kBalLists][32];
     __shared__ int s_some;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int team = warp / a.W;
-    const int pitch = (a.E + 3) & ~3, bufs = a.W == 1 ? 1 : 3;
-    float* adds = reinterpret_cast<float*>(bal_smem + (BAL ? bal_ring_bytes<NV>(a.W * a.teams, a.ring) : 0));
-    float* add0 = adds + static_cast<size_t>(team) * bufs * pitch;
-    Team tm{red[team], a.W, 1 + team, warp % a.W, lane, 0};
+    const int teams_warps = a.W * a.teams;
+    float* adds = reinterpret_cast<float*>(bal_smem + (BAL ? bal_ring_bytes<NV>(teams_warps, a.ring) : 0));
     const int64_t c0 = static_cast<int64_t>(blockIdx.x) * a.tokens;
     const int t0 = static_cast<int>(min(c0, static_cast<int64_t>(a.T)));
     const int t1 = static_cast<int>(min(c0 + a.tokens, static_cast<int64_t>(a.T)));
-    for (int e = threadIdx.x; e < a.teams * bufs * pitch; e += blockDim.x) adds[e] = 0.0f;
+    for (int e = threadIdx.x; e < teams_warps * NV * 128; e += blockDim.x) adds[e] = 0.0f;
     for (int i = threadIdx.x; i < kBalGradWarps * kBalRing; i += blockDim.x) mbar_init(&bars[i], 1);
+    for (int i = threadIdx.x; i < kBalGradWarps * kBalLists; i += blockDim.x) {
+        mbar_init(&list_full[i / kBalLists][i % kBalLists], 1);
+        mbar_init(&list_empty[i / kBalLists][i % kBalLists], a.W);
+    }
     if (threadIdx.x == 0) s_some = 0;
     fence_mbar_init();
     __syncthreads();
     griddep_wait();
     griddep_launch();
-    RowFeed<NV, VEC> feed;
-    RowMask mask;
-    mask.start(a, lane, t0 + team, t1);
+    const int G = bal_group(a.k), batch = 32 / G;
     float unit = 0.0f;
     if constexpr (BAL) {
-        feed.start(a, tm, warp, t0 + team, t1, bal_smem, bars);
         int some = 0;
         for (int q = threadIdx.x; q < a.Q; q += blockDim.x) some += a.seq_tokens_in[q] > 0;
         if (some) atomicAdd(&s_some, some);
@@ -692,58 +825,34 @@ __global__ void __launch_bounds__(kBalGradWarps * 32, 1) gate_grad_kernel(const 
                static_cast<float>(s_some > 0 ? s_some : 1);
     }
 
+    if (warp >= teams_warps) {
+        const int g = warp - teams_warps;
+        volatile uint8_t* tags = reinterpret_cast<uint8_t*>(adds + teams_warps * NV * 128) + g * 2 * batch * kBalTags;
+        if (a.teams > 2 * kBalGateWarps)
+            gate_lists<4>(a, g, t0, t1, tags, list, list_full, list_empty);
+        else if (a.teams > kBalGateWarps)
+            gate_lists<2>(a, g, t0, t1, tags, list, list_full, list_empty);
+        else
+            gate_lists<1>(a, g, t0, t1, tags, list, list_full, list_empty);
+        return;
+    }
+
+    const int team = warp / a.W;
+    Team tm{red[team], a.W, 1 + team, warp % a.W, lane, 0};
+    float* add = adds + static_cast<size_t>(warp) * NV * 128;      // this warp's part of a row
+    RowFeed<NV, VEC> feed;
+    RowMask mask;
+    mask.start(a, lane, t0 + team, t1);
+    if constexpr (BAL) feed.start(a, tm, warp, t0 + team, t1, bal_smem, bars);
+    const bool gate = a.grad_w != nullptr;
+    bool dead = false;
     int q = BAL ? first_sequence(a, t0) : a.Q, q_lo = 0, q_hi = -1;
     float2 g[NE / 2];
 #pragma unroll
     for (int i = 0; i < NE / 2; ++i) g[i] = make_float2(0.0f, 0.0f);
-
-    // this warp's turns at the gate: rows wt, wt + W, ... of the team
-    const bool gate = a.grad_w != nullptr;
-    const int turn = a.W * a.teams;
-    int tg = t0 + team + tm.wt * a.teams;          // token of this warp's next turn
-    // what a fetch leaves is only looked at a turn later, so no load is waited for where it starts
-    auto fetch_pick = [&](int64_t t, int& d, int& m) {
-        d = -1, m = 0;
-        if (gate && t < t1 && lane < a.k) {
-            d = a.ids[static_cast<size_t>(t) * a.k + lane];
-            m = a.mask[t];
-        }
-    };
-    auto picked = [&](int d, int m) { return m != 0 && d >= 0 && d < a.E ? d : -1; };   // -1: none
-    auto fetch_values = [&](int64_t t, int d, float& x, float& w) {
-        x = 0.0f, w = 0.0f;
-        if (d >= 0) {
-            x = a.logits[static_cast<size_t>(t) * a.E + d];
-            w = a.grad_w[static_cast<size_t>(t) * a.k + lane];
-        }
-    };
-    int id, id1, m1;
-    float xj, dw;
-    fetch_pick(tg, id, m1);
-    id = picked(id, m1);
-    fetch_values(tg, id, xj, dw);
-    fetch_pick(static_cast<int64_t>(tg) + turn, id1, m1);
-    int old_id = -1;                // this lane's entry of the warp's last turn, not yet cleared
-    float* old_buf = add0;
-    auto take_turn = [&](int buf) {
-        int id2, m2;
-        float xj1, dw1;
-        id1 = picked(id1, m1);
-        fetch_pick(static_cast<int64_t>(tg) + 2 * static_cast<int64_t>(turn), id2, m2);
-        fetch_values(static_cast<int64_t>(tg) + turn, id1, xj1, dw1);
-        if (__any_sync(0xffffffffu, id >= 0)) {
-            const float d = gate_pick_grad(id, xj, dw);
-            __syncwarp();       // behind the lanes that cleared this buffer
-            if (id >= 0) add0[buf * pitch + id] = d;
-        }
-        old_id = id, old_buf = add0 + buf * pitch;
-        id = id1, id1 = id2, m1 = m2, xj = xj1, dw = dw1;
-        tg += turn;
-    };
-
-    int row = 0, rbuf = 0, whose = 0;      // row of the team, its buffer, and the warp whose turn it was
-    if (gate && a.W > 1 && tm.wt == 0 && t0 + team < t1) take_turn(0);
-    for (int t = t0 + team; t < t1; t += a.teams, ++row) {
+    int slot = 0, phase = 0, in_batch = 0;
+    float* out = a.grad + static_cast<size_t>(t0 + team < t1 ? t0 + team : 0) * a.E;
+    for (int t = t0 + team; t < t1; t += a.teams, out += static_cast<size_t>(a.teams) * a.E) {
         const bool valid = mask.next();
         bool in_seq = false;
         float2 x[NE / 2];
@@ -766,7 +875,24 @@ __global__ void __launch_bounds__(kBalGradWarps * 32, 1) gate_grad_kernel(const 
             }
             in_seq = valid && t >= q_lo;
         }
-        if (gate && a.W == 1) take_turn(0);
+        // this row's entries that fall to this warp
+        int at = -1;
+        if (gate) {
+            if (in_batch == 0 && !dead)
+                dead = !mbar_wait_bounded(&list_full[team][slot], static_cast<uint32_t>(phase), kBalTimeout);
+            int2 entry = make_int2(-1, 0);
+            if (lane < G) entry = list[team][slot][in_batch * G + lane];
+            __syncwarp();       // also: behind the lanes that cleared the last row's entries
+            if (++in_batch == batch) {
+                in_batch = 0;
+                if (lane == 0) mbar_arrive(&list_empty[team][slot]);
+                if (++slot == kBalLists) slot = 0, phase ^= 1;
+            }
+            at = entry.x - tm.wt * NV * 128;
+            if (entry.x < 0 || at >= NV * 128) at = -1;
+            if (at >= 0) add[at] = __int_as_float(entry.y);
+            __syncwarp();
+        }
         float2 S2 = make_float2(0.0f, 0.0f), G2 = S2;
         if (BAL && in_seq) {
             float2 sum = make_float2(0.0f, 0.0f), dot = sum;
@@ -798,15 +924,12 @@ __global__ void __launch_bounds__(kBalGradWarps * 32, 1) gate_grad_kernel(const 
                 all = tm.sum(all);
             }
             const float S = all.x == 0.0f ? 0.0f : __frcp_rn(all.x);
-            const float G = all.y * S;
-            S2 = make_float2(S, S), G2 = make_float2(-G, -G);
+            const float G1 = all.y * S;
+            S2 = make_float2(S, S), G2 = make_float2(-G1, -G1);
         } else {
-            tm.sync();      // makes the row's entries visible to the team
 #pragma unroll
             for (int i = 0; i < NE / 2; ++i) x[i] = make_float2(0.0f, 0.0f);
         }
-        const float* add = add0 + rbuf * pitch;
-        float* out = a.grad + static_cast<size_t>(t) * a.E;
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
             const float2 lo = mul2(x[2 * v], S2), gl = add2(g[2 * v], G2);
@@ -814,7 +937,7 @@ __global__ void __launch_bounds__(kBalGradWarps * 32, 1) gate_grad_kernel(const 
             if constexpr (VEC) {
                 const int e = bal_expert<NV, VEC>(tm.wt, lane, 4 * v);
                 if (e < a.E) {
-                    const float4 z = *reinterpret_cast<const float4*>(add + e);
+                    const float4 z = *reinterpret_cast<const float4*>(add + 128 * v + 4 * lane);
                     const float2 p = fma2(lo, gl, make_float2(z.x, z.y)), r = fma2(hi, gh, make_float2(z.z, z.w));
                     __stcs(reinterpret_cast<float4*>(out + e), make_float4(p.x, p.y, r.x, r.y));
                 }
@@ -823,32 +946,19 @@ __global__ void __launch_bounds__(kBalGradWarps * 32, 1) gate_grad_kernel(const 
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int e = bal_expert<NV, VEC>(tm.wt, lane, 4 * v + i);
-                    if (e < a.E) __stcs(out + e, w[i] + add[e]);
+                    if (e < a.E) __stcs(out + e, w[i] + add[(4 * v + i) * 32 + lane]);
                 }
             }
         }
-        if (a.W == 1) {
-            __syncwarp();
-            if (old_id >= 0) old_buf[old_id] = 0.0f;
-        } else if (gate) {
-            // The warp that formed the row before this one clears it: at this row's barrier every warp had read it.
-            // The next warp in turn fills the row behind this one; its buffer was cleared a row ago.
-            const int next_buf = rbuf == 2 ? 0 : rbuf + 1;
-            const int prev = whose == 0 ? a.W - 1 : whose - 1, then = whose == a.W - 1 ? 0 : whose + 1;
-            if (tm.wt == prev && row > 0) {
-                if (old_id >= 0) old_buf[old_id] = 0.0f;
-                old_id = -1;
-            }
-            if (tm.wt == then && t + a.teams < t1) take_turn(next_buf);
-            rbuf = next_buf, whose = then;
-        }
+        __syncwarp();
+        if (at >= 0) add[at] = 0.0f;
     }
     if constexpr (BAL) feed.drain();
 }
 
 template <typename F>
 cudaError_t bal_launch(F* kernel, int ctas, int threads, size_t smem, int cluster, const BalArgs& a, cudaStream_t s) {
-    if (smem > 40 * 1024) {      // with the kernel's static shared memory above the 48 KB of an unset limit
+    if (smem > 24 * 1024) {      // with the kernel's static shared memory above the 48 KB of an unset limit
         const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel),
                                                    cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
         if (e != cudaSuccess) return e;
@@ -892,9 +1002,10 @@ cudaError_t launch_balance_main(const BalPlan& p, const BalArgs& a, cudaStream_t
 }
 template <int NV, bool VEC, bool BAL>
 cudaError_t launch_gate_grad_nv(const BalPlan& p, const BalArgs& a, cudaStream_t s) {
-    const int warps = p.W * p.teams;
-    const size_t smem = (BAL ? bal_ring_bytes<NV>(warps, p.ring) : 0) + static_cast<size_t>(p.teams) * (p.W == 1 ? 1 : 3) * ((a.E + 3) & ~3) * 4;
-    return bal_launch(gate_grad_kernel<NV, VEC, BAL>, p.ctas, warps * 32, smem, 1, a, s);
+    const int warps = p.W * p.teams, gate = a.grad_w != nullptr ? kBalGateWarps : 0;
+    const size_t smem = (BAL ? bal_ring_bytes<NV>(warps, p.ring) : 0) + static_cast<size_t>(warps) * NV * 512 +
+                        static_cast<size_t>(gate) * 2 * (32 / bal_group(a.k)) * kBalTags;
+    return bal_launch(gate_grad_kernel<NV, VEC, BAL>, p.ctas, (warps + gate) * 32, smem, 1, a, s);
 }
 template <bool VEC, bool BAL>
 cudaError_t launch_gate_grad(const BalPlan& p, const BalArgs& a, cudaStream_t s) {
