@@ -182,17 +182,28 @@ def _want(t: torch.Tensor, dtype: torch.dtype, name: str) -> None:
         raise ValueError(f"{name}: expected a contiguous tensor")
 
 
-def _at(t: Optional[torch.Tensor]) -> Optional[int]:
-    return None if t is None else t.data_ptr()
+def _device(t: torch.Tensor, dtype: torch.dtype, name: str) -> int:
+    """Index of the device of a call's first tensor."""
+    dev = t.get_device()
+    if dev < 0:
+        _want(t, dtype, name)      # raises
+    return dev
 
 
-def _enqueue(name: str, tensors, stream, *args) -> None:
-    """The call ``name(*args, stream)`` with the tensors' device as the current
-    one (they must share it); ``stream`` None is that device's current stream."""
-    dev = tensors[0].get_device()
-    for t in tensors:
-        if t is not None and t.get_device() != dev:
-            raise ValueError(f"{name}: tensors on devices {dev} and {t.get_device()}")
+def _take(t: Optional[torch.Tensor], dtype: torch.dtype, dev: int, name: str) -> Optional[int]:
+    """Address of a tensor after the checks of _want and that it is on device
+    ``dev`` (one call a tensor: the checks are much of a small call's time)."""
+    if t is None:
+        return None
+    if t.dtype is dtype and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
+    _want(t, dtype, name)
+    raise ValueError(f"{name}: on device {t.get_device()}, expected {dev}")
+
+
+def _enqueue(name: str, dev: int, stream, *args) -> None:
+    """The call ``name(*args, stream)`` with device ``dev`` as the current one;
+    ``stream`` None is that device's current stream."""
     fn = getattr(_lib or load(), name)
     if dev == torch._C._cuda_getDevice():
         status = fn(*args, _raw_stream(dev) if stream is None else stream.cuda_stream)
@@ -496,18 +507,16 @@ def balance_workspace_size(T: int, E: int, Q: int = 1) -> int:
 
 
 def _router_batch(fn, logits, topk_ids, token_mask, seq_offsets):
-    """-> (T, E, k, Q) of a router batch, checked."""
-    _want(logits, torch.float32, "logits")
-    _want(topk_ids, torch.int32, "topk_ids")
-    _want(token_mask, torch.uint8, "token_mask")
+    """-> (T, E, k, Q, device, addresses) of a router batch, checked."""
+    dev = _device(logits, torch.float32, "logits")
+    at = (_take(logits, torch.float32, dev, "logits"), _take(topk_ids, torch.int32, dev, "topk_ids"),
+          _take(token_mask, torch.uint8, dev, "token_mask"), _take(seq_offsets, torch.int32, dev, "seq_offsets"))
     T, E = logits.shape
-    Q = 1
-    if seq_offsets is not None:
-        _want(seq_offsets, torch.int32, "seq_offsets")
-        Q = seq_offsets.numel() - 1
-    if topk_ids.dim() != 2 or topk_ids.shape[0] != T or token_mask.numel() != T or Q < 1:
+    rows, k = topk_ids.shape
+    Q = 1 if seq_offsets is None else seq_offsets.numel() - 1
+    if rows != T or token_mask.numel() != T or Q < 1:
         raise ValueError(f"{fn}: shape mismatch")
-    return T, E, topk_ids.shape[1], Q
+    return T, E, k, Q, dev, at
 
 
 @_traced
@@ -523,31 +532,31 @@ def moe_balance_loss(logits: torch.Tensor, topk_ids: torch.Tensor, token_mask: t
     ``workspace`` is a uint8 CUDA tensor of at least ``balance_workspace_size``
     bytes (0 for small batches); when omitted, one is allocated here."""
     fn = "moe_balance_loss"
-    T, E, k, Q = _router_batch(fn, logits, topk_ids, token_mask, seq_offsets)
-    dev = logits.device
+    T, E, k, Q, dev, (at_logits, at_ids, at_mask, at_offsets) = _router_batch(fn, logits, topk_ids, token_mask,
+                                                                              seq_offsets)
+    where = logits.device
     if loss is None:
-        loss = torch.empty(1, dtype=torch.float32, device=dev)
+        loss = torch.empty(1, dtype=torch.float32, device=where)
     if counts is None:
-        counts = torch.empty(Q, E, dtype=torch.int32, device=dev)
+        counts = torch.empty(Q, E, dtype=torch.int32, device=where)
+    elif counts.shape != (Q, E):
+        raise ValueError(f"{fn}: shape mismatch")
     if prob_sums is None:
-        prob_sums = torch.empty(Q, E, dtype=torch.float32, device=dev)
+        prob_sums = torch.empty(Q, E, dtype=torch.float32, device=where)
+    elif prob_sums.shape != (Q, E):
+        raise ValueError(f"{fn}: shape mismatch")
     if seq_tokens is None:
-        seq_tokens = torch.empty(Q, dtype=torch.int32, device=dev)
+        seq_tokens = torch.empty(Q, dtype=torch.int32, device=where)
+    if loss.numel() != 1 or seq_tokens.numel() != Q:
+        raise ValueError(f"{fn}: shape mismatch")
     if workspace is None:
         need = load().moe_balance_workspace_size(T, E, Q)
         if need > 0:
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    else:
-        _want(workspace, torch.uint8, "workspace")
-    _want(loss, torch.float32, "loss")
-    _want(counts, torch.int32, "counts")
-    _want(prob_sums, torch.float32, "prob_sums")
-    _want(seq_tokens, torch.int32, "seq_tokens")
-    if loss.numel() != 1 or counts.shape != (Q, E) or prob_sums.shape != (Q, E) or seq_tokens.numel() != Q:
-        raise ValueError(f"{fn}: shape mismatch")
-    _enqueue(fn, (logits, topk_ids, token_mask, loss, counts, prob_sums, seq_tokens, workspace, seq_offsets), stream,
-             _at(logits), _at(topk_ids), _at(token_mask), T, E, k, _at(seq_offsets), Q, coeff, _at(loss), _at(counts),
-             _at(prob_sums), _at(seq_tokens), _at(workspace), 0 if workspace is None else workspace.numel())
+            workspace = torch.empty(need, dtype=torch.uint8, device=where)
+    _enqueue(fn, dev, stream, at_logits, at_ids, at_mask, T, E, k, at_offsets, Q, coeff,
+             _take(loss, torch.float32, dev, "loss"), _take(counts, torch.int32, dev, "counts"),
+             _take(prob_sums, torch.float32, dev, "prob_sums"), _take(seq_tokens, torch.int32, dev, "seq_tokens"),
+             _take(workspace, torch.uint8, dev, "workspace"), 0 if workspace is None else workspace.numel())
     return loss, counts, prob_sums, seq_tokens
 
 
@@ -562,27 +571,23 @@ def moe_route_backward(logits: torch.Tensor, topk_ids: torch.Tensor, token_mask:
     moe_balance_loss's loss, float32 [1]; with that call's coeff, counts,
     seq_tokens and seq_offsets), or from both."""
     fn = "moe_route_backward"
-    T, E, k, Q = _router_batch(fn, logits, topk_ids, token_mask, seq_offsets)
-    if grad_weights is not None:
-        _want(grad_weights, torch.float32, "grad_weights")
-        if grad_weights.shape != (T, k):
-            raise ValueError(f"{fn}: shape mismatch")
+    T, E, k, Q, dev, (at_logits, at_ids, at_mask, at_offsets) = _router_batch(fn, logits, topk_ids, token_mask,
+                                                                              seq_offsets)
+    if grad_weights is not None and grad_weights.shape != (T, k):
+        raise ValueError(f"{fn}: shape mismatch")
     if grad_loss is not None:
         if counts is None or seq_tokens is None:
             raise ValueError(f"{fn}: grad_loss needs counts and seq_tokens")
-        _want(grad_loss, torch.float32, "grad_loss")
-        _want(counts, torch.int32, "counts")
-        _want(seq_tokens, torch.int32, "seq_tokens")
         if grad_loss.numel() != 1 or counts.shape != (Q, E) or seq_tokens.numel() != Q:
             raise ValueError(f"{fn}: shape mismatch")
     if grad_logits is None:
-        grad_logits = torch.empty(T, E, dtype=torch.float32, device=logits.device)
-    _want(grad_logits, torch.float32, "grad_logits")
-    if grad_logits.shape != (T, E):
+        grad_logits = torch.empty_like(logits)
+    elif grad_logits.shape != (T, E):
         raise ValueError(f"{fn}: shape mismatch")
-    _enqueue(fn, (logits, topk_ids, token_mask, grad_logits, grad_weights, grad_loss, counts, seq_tokens, seq_offsets),
-             stream, _at(logits), _at(topk_ids), _at(token_mask), T, E, k, _at(grad_weights), _at(grad_loss), coeff,
-             _at(counts), _at(seq_tokens), _at(seq_offsets), Q, _at(grad_logits))
+    _enqueue(fn, dev, stream, at_logits, at_ids, at_mask, T, E, k,
+             _take(grad_weights, torch.float32, dev, "grad_weights"), _take(grad_loss, torch.float32, dev, "grad_loss"),
+             coeff, _take(counts, torch.int32, dev, "counts"), _take(seq_tokens, torch.int32, dev, "seq_tokens"),
+             at_offsets, Q, _take(grad_logits, torch.float32, dev, "grad_logits"))
     return grad_logits
 
 
@@ -639,33 +644,27 @@ def lora_add(base: torch.Tensor, x: torch.Tensor, a: torch.Tensor, b: torch.Tens
     allocated, and so is ``workspace`` (uint8, ``lora_workspace_size`` bytes, 0 up
     to 256 tokens)."""
     fn = "lora_add"
-    bf16 = base.dtype == torch.bfloat16
-    _want(base, torch.bfloat16 if bf16 else torch.float32, "base")
-    _want(x, torch.bfloat16, "x")
-    _want(a, torch.bfloat16, "a")
-    _want(b, torch.bfloat16, "b")
-    _want(adapter_ids, torch.int32, "adapter_ids")
-    if scales is not None:
-        _want(scales, torch.float32, "scales")
+    bf16 = base.dtype is torch.bfloat16
+    dtype = torch.bfloat16 if bf16 else torch.float32
+    dev = _device(base, dtype, "base")
     T, H = x.shape
     L, R = a.shape[:2]
-    N = base.shape[1]
+    N = base.shape[-1]
     if a.shape != (L, R, H) or b.shape != (L, N, R) or base.shape != (T, N) or adapter_ids.numel() != T or (
             scales is not None and scales.numel() != L):
         raise ValueError(f"{fn}: shape mismatch")
     if out is None:
         out = torch.empty_like(base)
-    _want(out, base.dtype, "out")
-    if out.shape != base.shape:
+    elif out.shape != base.shape:
         raise ValueError(f"{fn}: shape mismatch")
     if workspace is None:
         need = load().lora_workspace_size(T, H, N, R, L)
         if need > 0:
             workspace = torch.empty(need, dtype=torch.uint8, device=base.device)
-    else:
-        _want(workspace, torch.uint8, "workspace")
-    _enqueue(fn, (base, x, a, b, adapter_ids, scales, out, workspace), stream, _at(base), int(bf16), _at(x), T, H,
-             _at(a), _at(b), N, R, L, _at(adapter_ids), _at(scales), _at(out), _at(workspace),
+    _enqueue(fn, dev, stream, _take(base, dtype, dev, "base"), bf16, _take(x, torch.bfloat16, dev, "x"), T, H,
+             _take(a, torch.bfloat16, dev, "a"), _take(b, torch.bfloat16, dev, "b"), N, R, L,
+             _take(adapter_ids, torch.int32, dev, "adapter_ids"), _take(scales, torch.float32, dev, "scales"),
+             _take(out, dtype, dev, "out"), _take(workspace, torch.uint8, dev, "workspace"),
              0 if workspace is None else workspace.numel())
     return out
 
