@@ -4,7 +4,9 @@
 #include <cstring>
 #include <cstdarg>
 #include <cstdio>
+#include <map>
 #include <mutex>
+#include <utility>
 
 #include "moe_boundary.h"
 #include "common.cuh"
@@ -52,6 +54,20 @@ const DeviceInfo& device_info() {
         g_info[dev].max_smem_optin = smem;
     });
     return g_info[dev];
+}
+
+cudaError_t allow_smem(const void* kernel, size_t bytes) {
+    static std::mutex lock;
+    static std::map<std::pair<const void*, int>, size_t> allowed;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    std::lock_guard<std::mutex> hold(lock);
+    size_t& most = allowed[{kernel, dev}];
+    if (bytes <= most) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+    if (e == cudaSuccess) most = bytes;
+    return e;
 }
 
 }  // namespace mb
@@ -339,15 +355,17 @@ int moe_dispatch(const int32_t* topk_ids, int T, int k, int expert_begin, int E,
                        fn);
 }
 
+// Whether two ranges of memory share a byte (false for a null pointer).
+static bool overlap(const void* p, size_t n, const void* q, size_t m) {
+    if (!p || !q) return false;
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+    return a < b + m && b < a + n;
+}
+
 // ------------------------------------------------------------------ low-rank adapters
 size_t lora_workspace_size(int T, int H, int N, int R, int L) {
     if (!moe_boundary_supported(MB_STAGE_LORA, T, H, N, R, L)) return 0;
     return lora_workspace_bytes(T, H, N, R, L);
-}
-
-static bool overlap(const void* p, size_t n, const void* q, size_t m) {
-    const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
-    return a < b + m && b < a + n;
 }
 
 int lora_add(const void* base, int base_bf16, const uint16_t* x, int T, int H, const uint16_t* a, const uint16_t* b,
@@ -368,7 +386,8 @@ int lora_add(const void* base, int base_bf16, const uint16_t* x, int T, int H, c
         return fail(MB_ERR_INVALID_ARG, "%s: pointers must be 16-byte aligned", fn);
     const size_t nout = static_cast<size_t>(T) * N * (base_bf16 ? 2 : 4), l = static_cast<size_t>(L) * R * 2;
     if ((out != base && overlap(out, nout, base, nout)) || overlap(out, nout, x, static_cast<size_t>(T) * H * 2) ||
-        overlap(out, nout, a, l * H) || overlap(out, nout, b, l * N))
+        overlap(out, nout, a, l * H) || overlap(out, nout, b, l * N) ||
+        overlap(out, nout, adapter_ids, static_cast<size_t>(T) * 4) || overlap(out, nout, scales, static_cast<size_t>(L) * 4))
         return fail(MB_ERR_INVALID_ARG, "%s: out overlaps an input (only out == base is allowed)", fn);
     const size_t need = lora_workspace_bytes(T, H, N, R, L);
     if (need > 0) {
@@ -376,6 +395,8 @@ int lora_add(const void* base, int base_bf16, const uint16_t* x, int T, int H, c
             return fail(MB_ERR_INVALID_ARG, "%s: needs a workspace of %zu bytes (got %zu)", fn, need,
                         workspace ? workspace_bytes : static_cast<size_t>(0));
         if (!aligned256(workspace)) return fail(MB_ERR_INVALID_ARG, "%s: workspace must be 256-byte aligned", fn);
+        if (overlap(workspace, need, out, nout) || overlap(workspace, need, base, nout))
+            return fail(MB_ERR_INVALID_ARG, "%s: workspace overlaps base or out", fn);
     }
     const LoraLaunch ll{base, out, base_bf16 != 0, x, a, b, adapter_ids, scales, T, H, N, R, L, workspace};
     return cuda_status(launch_lora_add(ll, static_cast<cudaStream_t>(stream)), fn);
@@ -438,7 +459,11 @@ int moe_route_backward(const float* logits, const int32_t* topk_ids, const uint8
         !aligned16(counts) || !aligned16(seq_tokens) || !aligned16(grad_logits) ||
         (reinterpret_cast<uintptr_t>(grad_loss) & 3u))
         return fail(MB_ERR_INVALID_ARG, "%s: pointers must be 16-byte aligned", fn);
-    if (grad_logits == logits) return fail(MB_ERR_INVALID_ARG, "%s: grad_logits must not be logits", fn);
+    const size_t rows = static_cast<size_t>(T) * E * 4, picks = static_cast<size_t>(T) * k * 4;
+    if (overlap(grad_logits, rows, logits, rows) || overlap(grad_logits, rows, topk_ids, picks) ||
+        overlap(grad_logits, rows, grad_weights, picks) || overlap(grad_logits, rows, token_mask, static_cast<size_t>(T)) ||
+        overlap(grad_logits, rows, counts, static_cast<size_t>(Q) * E * 4))
+        return fail(MB_ERR_INVALID_ARG, "%s: grad_logits overlaps an input", fn);
     const GateGradLaunch b{logits, topk_ids, token_mask, T, E, k, grad_weights, grad_loss, coeff, counts, seq_tokens,
                            seq_offsets, Q, grad_logits};
     return cuda_status(launch_route_backward(b, static_cast<cudaStream_t>(stream)), fn);

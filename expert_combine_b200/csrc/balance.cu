@@ -959,8 +959,7 @@ __global__ void __launch_bounds__((kBalGradWarps + kBalGateWarps) * 32, 1) gate_
 template <typename F>
 cudaError_t bal_launch(F* kernel, int ctas, int threads, size_t smem, int cluster, const BalArgs& a, cudaStream_t s) {
     if (smem > 24 * 1024) {      // with the kernel's static shared memory above the 48 KB of an unset limit
-        const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel),
-                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+        const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), smem);
         if (e != cudaSuccess) return e;
     }
     cudaLaunchConfig_t cfg = {};

@@ -13,6 +13,10 @@ struct DeviceInfo {
 };
 const DeviceInfo& device_info();   // current device, cached per device
 
+// Lets a kernel take `bytes` of dynamic shared memory on the current device; asks
+// the runtime only when no earlier call has allowed as much.
+cudaError_t allow_smem(const void* kernel, size_t bytes);
+
 // The exhaustive check of the router's fast sigmoid against the exact one.
 cudaError_t launch_fast_sigmoid_check(float* max_err, cudaStream_t s);
 cudaError_t launch_route(const float* logits, const float* bias, const uint8_t* mask, int T, int E,

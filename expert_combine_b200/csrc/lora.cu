@@ -1111,8 +1111,7 @@ cudaError_t launch_lora_many(const LoraLaunch& l, cudaStream_t s) {
     if (lm_one_plan(l.T, l.L)) {
         const void* plan = reinterpret_cast<const void*>(lora_plan_kernel);
         const size_t psmem = lm_plan_bytes(l.T, l.L);
-        e = cudaFuncSetAttribute(plan, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 static_cast<int>(lm_plan_bytes(kLmPlanTokens, kLmPlanAdapters)));
+        e = allow_smem(plan, psmem);
         if (e == cudaSuccess) e = lm_launch(plan, 1, 1024, psmem, targs, s);
     } else {
         e = launch_dispatch(l.ids, l.T, 1, 0, l.L, offsets, row_idx, row_token, w + at.dispatch, s);
@@ -1128,7 +1127,7 @@ cudaError_t launch_lora_many(const LoraLaunch& l, cudaStream_t s) {
     const void* expand = l.bf16 ? reinterpret_cast<const void*>(lora_expand_kernel<uint16_t>)
                                 : reinterpret_cast<const void*>(lora_expand_kernel<float>);
     for (const void* k : {shrink, expand}) {
-        e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        e = allow_smem(k, static_cast<size_t>(smem));
         if (e != cudaSuccess) return e;
     }
     void* sargs[] = {&amap, &a};

@@ -289,7 +289,8 @@ int moe_balance_loss(const float* logits, const int32_t* topk_ids, const uint8_t
  * the moe_balance_loss call, and unused when grad_loss is NULL.
  *
  *   grad_weights [T, k] FP32 or NULL     grad_loss [1] FP32 on the device or NULL
- *   grad_logits  [T, E] FP32 (out; every element is written; not logits)
+ *   grad_logits  [T, E] FP32 (out; every element is written; apart
+ *                from the inputs)
  * At least one of the two incoming gradients is given.  Supported: as
  * moe_balance_loss.
  */
@@ -352,7 +353,7 @@ int router_logits(const uint16_t* x, int T, int H, const uint16_t* w3, int E, fl
  *
  *   base  [T, N] FP32 or BF16 (base_bf16 = 0 or 1)    x  [T, H] BF16
  *   out   [T, N] of base's type (out): base itself (in place) or memory apart
- *         from base, x, a and b
+ *         from the inputs and the workspace
  *   a  [L, R, H] BF16       b  [L, N, R] BF16
  *   adapter_ids  [T] int32  scales  [L] FP32, or NULL for 1
  *   workspace  device scratch of lora_workspace_size(T, H, N, R, L) bytes,

@@ -45,8 +45,10 @@ def test_library_refuses_before_any_launch():
     # out is base itself or apart from every input
     shifted = ctypes.c_void_p((1 << 32) + 16)
     assert call(out=shifted) == 1 and "overlaps" in eb.last_error()
-    for name, p in (("x", x), ("a", a), ("b", b)):
+    for name, p in (("x", x), ("a", a), ("b", b), ("ids", ids)):
         assert call(out=p) == 1 and "overlaps" in eb.last_error(), name
+    assert call(scales=out) == 1 and "overlaps" in eb.last_error()
+    assert call(T=300, ws=out) == 1 and call(T=300, ws=base) == 1 and "workspace overlaps" in eb.last_error()
     assert eb.lora_workspace_size(4, 64, 32, 9, 2) == 0
     assert eb.supported(eb.STAGE_LORA, 1, 8192, 256, 16, 8) and not eb.supported(eb.STAGE_LORA, 1, 8192, 256, 256, 8)
     assert not eb.supported(eb.STAGE_LORA, 1, 64, 262144, 8, 4097)

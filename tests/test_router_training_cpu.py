@@ -89,14 +89,15 @@ def test_library_refuses_before_any_launch():
     assert eb.balance_workspace_size(4, 16, 1) == 0
     assert eb.balance_workspace_size(4, 5000, 1) == 0 and eb.balance_workspace_size(4, 16, 0) == 0
 
-    b = ctypes.c_void_p(0x2000)
+    b = ctypes.c_void_p(1 << 32)
 
     def back(T=4, E=16, k=2, ptr=a, dw=a, dl=a, counts=a, n=a, off=N, Q=1, out=b):
         return lib.moe_route_backward(ptr, ptr, ptr, T, E, k, dw, dl, 0.1, counts, n, off, Q, out, N)
     assert back(T=0) == 0                                       # empty: no launch
     assert back(dw=N, dl=N) == 1 and "neither" in eb.last_error()
     assert back(counts=N) == 1 and back(n=N) == 1 and back(out=N) == 1 and back(ptr=N) == 1
-    assert back(out=a) == 1 and "must not be" in eb.last_error()
+    for p in (a, ctypes.c_void_p(0x1000 + 16), ctypes.c_void_p(0x1000 - 16)):
+        assert back(out=p) == 1 and "overlaps" in eb.last_error()
     assert back(Q=2) == 1 and back(E=4097) == 2 and back(T=-1) == 1 and back(k=17) == 2
     assert back(ptr=odd) == 1 and back(dw=odd) == 1 and back(out=odd) == 1
     assert eb.supported(eb.STAGE_BALANCE, 8192, 0, 256, 8, 4) and not eb.supported(eb.STAGE_BALANCE, 1, 0, 4, 8, 1)
