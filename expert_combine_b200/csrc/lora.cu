@@ -22,22 +22,28 @@
 // order and forms its share of the columns with FP32 multiply-adds, two columns
 // a thread.  B and base are asked into L2 before the first product begins.
 //
-// Many tokens (prefill).  The tokens are grouped by adapter with the dispatch
-// of the routing entries (one "pick" a token, L "experts"), each adapter's run
-// is cut into tiles of 128 tokens, and both products run on the tensor cores
-// (tcgen05, accumulators in tensor memory), one persistent CTA per SM: a TMA
-// warp, an MMA thread and eight epilogue warps.
+// Many tokens (prefill).  The tokens are sorted by adapter (a one-CTA kernel, or
+// the dispatch of the routing entries for the larger batches: one "pick" a
+// token, L "experts"), each adapter's run is cut into tiles of 128 tokens, and
+// both products run on the tensor cores (tcgen05, accumulators in tensor
+// memory), one persistent CTA per SM: a TMA thread, an MMA thread, four loading
+// and eight epilogue warps.
 //   shrink  All tiles' steps of 128 k form one line that is cut into equal
 //     pieces, one per CTA, so the SMs finish together whatever the sizes of
 //     the groups.  The rows of a tile lie anywhere in x: four warps fetch them
-//     in 16-byte pieces.  A tile that several CTAs share is summed by the one that
-//     arrives last, from the partials, in the CTAs' order (an integer counter
-//     per tile; the sum's order does not depend on the arrival).  It writes v
-//     scaled and split into BF16 parts (3 for FP32 outputs: 2^-24 of v is left;
-//     2 for BF16 outputs: 2^-16), in the layout of the next MMA's operand.
-//   expand  Work items are a tile x 128 columns, cut the same way.  D = sum
-//     over the parts v_p B^T; base arrives in the swizzled layout in which an epilogue thread reads its row without bank conflicts, the sum
-//     replaces it there, and the warp writes whole 128-byte rows of out.
+//     in 16-byte pieces.  A tile that several CTAs share is summed by the one
+//     that arrives last, from the partials, in the CTAs' order (an integer
+//     counter per tile; the sum's order does not depend on the arrival).  It
+//     writes v scaled and split into BF16 parts (3 for FP32 outputs: 2^-24 of v
+//     is left; 2 for BF16 outputs: 2^-16), in the layout of the next MMA's
+//     operand.
+//   expand  Work items are a tile x 128 columns, cut the same way.  D = sum over
+//     the parts v_p B^T; base arrives in the swizzled layout in which an epilogue
+//     thread reads its row without bank conflicts, the sum replaces it there,
+//     and the warp writes whole 128-byte rows of out.
+// In steady state both move about 25 bytes a cycle and SM between L2 and the
+// SMs.  8192 tokens x 8192 -> 8192, rank 64, BF16: 95 us (x, base and out alone
+// are 61 at the copy rate); -> 256 columns, rank 32, FP32: 47 us.
 #include "internal.h"
 #include "common.cuh"
 #include "tmap.h"
