@@ -20,7 +20,7 @@
 // 16-byte load, and two MMAs use up the four words of each.  Then every CTA
 // reads the eight partial v through distributed shared memory, adds them in
 // order and forms its share of the columns with FP32 multiply-adds, two columns
-// a thread.  B and base are asked into L2 before the first product begins.
+// a thread.  B is asked into L2 before the first product begins.
 //
 // Many tokens (prefill).  The tokens are sorted by adapter (a one-CTA kernel, or
 // the dispatch of the routing entries for the larger batches: one "pick" a

@@ -162,6 +162,59 @@ def test_beside_the_router_projection(cuda_dev, T):
     assert int(n) == T and int(counts.sum()) == T * k and float(loss) > 0
 
 
+def _shifted(t):
+    """The same values at an address that is 16-byte aligned and no more."""
+    buf = torch.zeros(t.numel() + 64, dtype=t.dtype, device=t.device)
+    step = 16 // t.element_size()
+    at = next(k for k in range(step, 64, step) if (buf.data_ptr() + k * t.element_size()) % 32 == 16)
+    v = buf[at:at + t.numel()].view(t.shape)
+    v.copy_(t)
+    return v
+
+
+@pytest.mark.parametrize("T,bf16", [(30, False), (30, True), (500, False), (500, True)])
+def test_addresses_of_16_bytes(cuda_dev, T, bf16):
+    i = _inputs(cuda_dev, T, 520, 264, 24, 3, bf16, seed=12)
+    _check({k: _shifted(v) for k, v in i.items()}, out=_shifted(i["base"]))
+
+
+def test_two_streams_at_once(cuda_dev):
+    """Calls that overlap on the GPU, each with its own workspace, few and many tokens."""
+    cases = [_inputs(cuda_dev, T, 1024, 512, 16, 8, True, seed=T) for T in (64, 2000, 128, 3000)]
+    call = lambda i: eb.lora_add(i["base"], i["x"], i["a"], i["b"], i["adapter_ids"], scales=i["scales"])  # noqa: E731
+    want = [call(i) for i in cases]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    got = [[] for _ in cases]
+    for _ in range(5):
+        for s, i, g in zip(streams, cases, got):
+            with torch.cuda.stream(s):
+                g.append(call(i))
+    torch.cuda.synchronize()
+    assert all(torch.equal(w, x) for w, g in zip(want, got) for x in g)
+    assert eb.device_status() == 0
+
+
+def test_graphs_that_share_a_workspace(cuda_dev):
+    """Two captured calls with one workspace, replayed one after the other."""
+    i, j = (_inputs(cuda_dev, T, 512, 256, 16, 4, False, seed=T) for T in (700, 900))
+    ws = torch.empty(eb.lora_workspace_size(900, 512, 256, 16, 4), dtype=torch.uint8, device=cuda_dev)
+    call = lambda k, **kw: eb.lora_add(k["base"], k["x"], k["a"], k["b"], k["adapter_ids"], scales=k["scales"], **kw)  # noqa: E731
+    want = [call(i), call(j)]
+    outs = [torch.empty_like(w) for w in want]
+    graphs = []
+    for k, o in zip((i, j), outs):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            call(k, out=o, workspace=ws)
+        graphs.append(g)
+    for _ in range(3):
+        for g in graphs:
+            g.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(w, o) for w, o in zip(want, outs))
+
+
 def test_refusals(cuda_dev):
     i = _inputs(cuda_dev, 4, 64, 32, 8, 2, False)
     call = lambda **kw: eb.lora_add(**{**i, **kw})  # noqa: E731

@@ -221,6 +221,52 @@ def test_repeats_bit_for_bit_and_leaves_guards(cuda_dev):
     assert all(bool((buf[n][s:] == -77).all()) for n, s in sizes.items()) and bool((ws[need:] == 77).all())
 
 
+@pytest.mark.parametrize("T,E", [(40, 64), (3000, 128), (60, 2560)])
+def test_addresses_of_16_bytes(cuda_dev, T, E):
+    """Inputs and outputs at addresses that are 16-byte aligned and no more give the same bits."""
+    x, ids, mask, dw = _inputs(T, E, 4, seed=8)
+    tx, ti, tm, tw = _dev(cuda_dev, x, ids, mask, dw)
+
+    def shifted(t):
+        buf = torch.zeros(t.numel() + 64, dtype=t.dtype, device=cuda_dev)
+        step = 16 // t.element_size()
+        at = next(k for k in range(step, 64, step) if (buf.data_ptr() + k * t.element_size()) % 32 == 16)
+        buf[at:at + t.numel()].copy_(t.flatten())
+        return buf[at:at + t.numel()].view(t.shape)
+    one = torch.ones(1, device=cuda_dev)
+    out = []
+    for f in (lambda t: t, shifted):
+        b = tuple(f(t) for t in (tx, ti, tm))
+        loss, counts, probs, n = eb.moe_balance_loss(*b, 0.1)
+        out.append((loss, counts, probs, n, eb.moe_route_backward(*b, grad_weights=f(tw), grad_loss=one, coeff=0.1,
+                                                                  counts=f(counts), seq_tokens=f(n),
+                                                                  grad_logits=f(torch.zeros(T, E, device=cuda_dev)))))
+    torch.cuda.synchronize()
+    assert all(torch.equal(p, q) for p, q in zip(*out))
+
+
+def test_two_streams_at_once(cuda_dev):
+    """Calls that overlap on the GPU, one cluster and many CTAs."""
+    cases = [_dev(cuda_dev, *_inputs(T, E, 6, seed=T)) for T, E in ((100, 64), (4000, 256), (200, 512), (300, 2560))]
+    one = torch.ones(1, device=cuda_dev)
+
+    def step(x, ids, mask, dw):
+        loss, counts, probs, n = eb.moe_balance_loss(x, ids, mask, 0.1)
+        return loss, counts, probs, n, eb.moe_route_backward(x, ids, mask, grad_weights=dw, grad_loss=one, coeff=0.1,
+                                                             counts=counts, seq_tokens=n)
+    want = [step(*c) for c in cases]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    got = [[] for _ in cases]
+    for _ in range(5):
+        for s, c, g in zip(streams, cases, got):
+            with torch.cuda.stream(s):
+                g.append(step(*c))
+    torch.cuda.synchronize()
+    assert all(torch.equal(p, q) for w, g in zip(want, got) for r in g for p, q in zip(w, r))
+    assert eb.device_status() == 0
+
+
 def test_no_tokens(cuda_dev):
     z = lambda *s, dt=torch.float32: torch.zeros(*s, dtype=dt, device=cuda_dev)  # noqa: E731
     off = z(3, dt=torch.int32)
