@@ -56,7 +56,7 @@ const DeviceInfo& device_info() {
     return g_info[dev];
 }
 
-cudaError_t allow_smem(const void* kernel, size_t bytes) {
+cudaError_t allow_smem(const void* kernel, size_t bytes) try {
     static std::mutex lock;
     static std::map<std::pair<const void*, int>, size_t> allowed;
     int dev = 0;
@@ -68,6 +68,8 @@ cudaError_t allow_smem(const void* kernel, size_t bytes) {
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
     if (e == cudaSuccess) most = bytes;
     return e;
+} catch (...) {      // no exception leaves a C entry point
+    return cudaErrorMemoryAllocation;
 }
 
 }  // namespace mb

@@ -276,6 +276,7 @@ constexpr int kLmSlabBytes = kLmTile * 128;  // 16 KB
 constexpr int kLmCols = 128;                 // columns of out per work item
 constexpr int kLmThreads = 16 * 32;          // TMA, MMA, 2 warps that copy rows without an adapter, 8 epilogue, 4 loading
 constexpr int kLmLoadWarp = 12;              // first of the warps that gather rows
+constexpr int kLmCtas = 148;                 // most CTAs of the two kernels; the workspace has a slot for each
 constexpr int kLmPlanTokens = 32768;         // most tokens and adapters the one-CTA plan takes
 constexpr int kLmPlanAdapters = 1024;
 constexpr int kLmEpiWarps = 8;
@@ -295,7 +296,7 @@ struct LmArgs {
     LmTile* tiles;
     int32_t* ntiles;             // [1]
     int32_t* arrived;            // [tiles] CTAs that have left their partial
-    float* part;                 // [SMs + tiles][R][128]
+    float* part;                 // [CTAs + tiles][R][128]
     uint16_t* v;                 // [tiles][parts][ks][128][64]
     const uint16_t* x;
     const float* scales;
@@ -1058,7 +1059,7 @@ LmLayout lm_layout(int T, int H, int R, int L) {
     l.tiles = take(nt * sizeof(LmTile));
     l.ntiles = take(4);
     l.arrived = take(nt * 4);
-    l.part = take((nt + static_cast<size_t>(device_info().sm_count)) * R * kLmTile * 4);
+    l.part = take((nt + kLmCtas) * R * kLmTile * 4);
     l.v = take(nt * 3 * ks * kLmSlabBytes);
     l.bytes = at;
     return l;
@@ -1136,11 +1137,12 @@ cudaError_t launch_lora_many(const LoraLaunch& l, cudaStream_t s) {
         e = allow_smem(k, static_cast<size_t>(smem));
         if (e != cudaSuccess) return e;
     }
+    const int ctas = device_info().sm_count < kLmCtas ? device_info().sm_count : kLmCtas;
     void* sargs[] = {&amap, &a};
-    e = lm_launch(shrink, device_info().sm_count, kLmThreads, smem, sargs, s);
+    e = lm_launch(shrink, ctas, kLmThreads, smem, sargs, s);
     if (e != cudaSuccess) return e;
     void* eargs[] = {&vmap, &bmap, &a};
-    return lm_launch(expand, device_info().sm_count, kLmThreads, smem, eargs, s);
+    return lm_launch(expand, ctas, kLmThreads, smem, eargs, s);
 }
 
 }  // namespace

@@ -98,11 +98,12 @@ def test_in_place_without_scales_and_guards(cuda_dev, T):
     assert torch.equal(y[i["adapter_ids"] < 0], i["base"][i["adapter_ids"] < 0])
 
 
-@pytest.mark.parametrize("T", [40, 600])
-def test_unused_values_do_not_leak(cuda_dev, T):
+@pytest.mark.parametrize("T,N,R", [(40, 128, 16), (600, 128, 16), (40, 136, 8), (600, 136, 8), (600, 136, 24),
+                                   (600, 200, 72)])
+def test_unused_values_do_not_leak(cuda_dev, T, N, R):
     """NaN in x of tokens without an adapter, in an adapter nobody uses, and in one token's x stay where they are."""
     ids = [(-1, 0, 2, 2, 0)[t % 5] for t in range(T)]
-    i = _inputs(cuda_dev, T, 512, 128, 16, 4, False, seed=8, ids=ids)
+    i = _inputs(cuda_dev, T, 512, N, R, 4, False, seed=8, ids=ids)
     want, tol = _reference(i)
     i["x"][0::5] = float("nan")
     i["a"][1] = float("nan")
