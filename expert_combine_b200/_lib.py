@@ -641,8 +641,8 @@ def lora_add(base: torch.Tensor, x: torch.Tensor, a: torch.Tensor, b: torch.Tens
 
     base and out are float32 or bfloat16, x [T, H], a [L, R, H] and b [L, N, R]
     bfloat16.  ``out=base`` works in place; without ``out`` a tensor is
-    allocated, and so is ``workspace`` (uint8, ``lora_workspace_size`` bytes, 0 up
-    to 256 tokens)."""
+    allocated, and so is ``workspace`` (uint8, ``lora_workspace_size`` bytes, 0
+    for few tokens)."""
     fn = "lora_add"
     bf16 = base.dtype is torch.bfloat16
     dtype = torch.bfloat16 if bf16 else torch.float32

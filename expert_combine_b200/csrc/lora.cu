@@ -55,7 +55,9 @@ namespace {
 
 constexpr int kLoraThreads = 256;
 constexpr int kLoraWarps = kLoraThreads / 32;
-constexpr int kLoraTokens = 256;           // most tokens of this path
+constexpr int kLoraTokens = 256;           // most tokens of this path,
+constexpr int kLoraTokensWide = 192;       // and of more than kLoraNarrow ranks, see lora_few
+constexpr int kLoraNarrow = 32;
 constexpr int kLoraGroup = 8;              // tokens per group
 constexpr int kLoraCluster = 8;            // CTAs per group
 
@@ -282,7 +284,10 @@ constexpr int kLmPlanAdapters = 1024;
 constexpr int kLmEpiWarps = 8;
 constexpr int kLmBytes = 208 * 1024;         // ring buffers of a CTA
 constexpr int kLmMaxStages = 12;
-constexpr int kLmChain = 8;                  // steps (of 2 slabs) the shrink adds up in tensor memory, see below
+// Fewest steps worth a CTA of the shrink: the CTA that adds a tile's partials waits for each four of them (256
+// tokens of one adapter, rank 64, 8192 -> 8192: 31 us with 8, 45 with 1; 8192 tokens: the same).
+constexpr int kLmLeast = 8;
+constexpr int kLmChain = 4;                  // steps (of 2 slabs) the shrink adds up in tensor memory, see below
 constexpr unsigned int kLmTimeout = 32u;     // bit 5 of the device status word
 
 struct LmTile {
@@ -543,8 +548,8 @@ __device__ __forceinline__ void lm_write_v(const LmArgs& a, int tile, int gi, in
 
 // The tensor core cuts off what its FP32 accumulator cannot hold, always
 // towards zero, so a long chain of MMAs drifts (512 of them, H = 8192: 1.7e-6 of
-// the result in the mean).  After kLmChain steps (64 MMAs) the accumulator is
-// added to registers with ordinary rounding: 6e-7.  GH: groups of 16 ranks of
+// the result in the mean; 64 of them: 6e-7).  After kLmChain steps (32 MMAs) the
+// accumulator is added to registers with ordinary rounding: 2e-7.  GH: groups of 16 ranks of
 // an epilogue thread (the eight warps halve the ranks).
 template <int GH>
 __global__ void __launch_bounds__(kLmThreads, 1) lora_shrink_kernel(const __grid_constant__ CUtensorMap amap,
@@ -583,7 +588,8 @@ __global__ void __launch_bounds__(kLmThreads, 1) lora_shrink_kernel(const __grid
     griddep_launch();
 
     const int J = (a.H + kLmStep * kLmSlab - 1) / (kLmStep * kLmSlab);   // steps of a tile
-    const int64_t U = static_cast<int64_t>(*a.ntiles) * J, G = min(static_cast<int64_t>(gridDim.x), U);
+    const int64_t U = static_cast<int64_t>(*a.ntiles) * J;
+    const int64_t G = min(static_cast<int64_t>(gridDim.x), max(U / kLmLeast, min(U, static_cast<int64_t>(1))));
     const bool works = blockIdx.x < G;       // every working CTA has at least one step
     const int64_t u0 = works ? U * blockIdx.x / G : 0, u1 = works ? U * (blockIdx.x + 1) / G : 0;
 
@@ -1147,12 +1153,19 @@ cudaError_t launch_lora_many(const LoraLaunch& l, cudaStream_t s) {
 
 }  // namespace
 
+// Whether the one-launch path takes a batch: as far as its CTAs' threads look at
+// the tokens, and with many ranks, whose columns its FP32 multiply-adds form,
+// not quite so far (8192 -> 8192 on the GPU, few against many: rank 64, 128
+// tokens 29 against 33 us, 256 tokens 47 against 31; rank 16, 256 tokens 16
+// against 27).
+static bool lora_few(int T, int R) { return T <= (R <= kLoraNarrow ? kLoraTokens : kLoraTokensWide); }
+
 size_t lora_workspace_bytes(int T, int H, int N, int R, int L) {
-    return T > kLoraTokens ? lm_layout(T, H, R, L).bytes : 0;
+    return lora_few(T, R) ? 0 : lm_layout(T, H, R, L).bytes;
 }
 
 cudaError_t launch_lora_add(const LoraLaunch& l, cudaStream_t s) {
-    if (l.T > kLoraTokens) return launch_lora_many(l, s);
+    if (!lora_few(l.T, l.R)) return launch_lora_many(l, s);
     LoraArgs a{};
     a.T = l.T, a.H = l.H, a.N = l.N, a.R = l.R, a.L = l.L;
     a.x = l.x, a.a = l.a, a.b = l.b, a.ids = l.ids, a.scales = l.scales, a.base = l.base, a.out = l.out;
