@@ -284,8 +284,9 @@ constexpr int kLmPlanAdapters = 1024;
 constexpr int kLmEpiWarps = 8;
 constexpr int kLmBytes = 208 * 1024;         // ring buffers of a CTA
 constexpr int kLmMaxStages = 12;
-// Fewest steps worth a CTA of the shrink: the CTA that adds a tile's partials waits for each four of them (256
-// tokens of one adapter, rank 64, 8192 -> 8192: 31 us with 8, 45 with 1; 8192 tokens: the same).
+// Fewest steps worth a CTA of the shrink: the CTA that adds a tile's partials
+// waits for each four of them (64 tokens of one adapter, rank 128, 8192 -> 256:
+// 30 us with 8 steps, 62 with 1; 8192 tokens: the same).
 constexpr int kLmLeast = 8;
 constexpr int kLmChain = 4;                  // steps (of 2 slabs) the shrink adds up in tensor memory, see below
 constexpr unsigned int kLmTimeout = 32u;     // bit 5 of the device status word
@@ -549,8 +550,8 @@ __device__ __forceinline__ void lm_write_v(const LmArgs& a, int tile, int gi, in
 // The tensor core cuts off what its FP32 accumulator cannot hold, always
 // towards zero, so a long chain of MMAs drifts (512 of them, H = 8192: 1.7e-6 of
 // the result in the mean; 64 of them: 6e-7).  After kLmChain steps (32 MMAs) the
-// accumulator is added to registers with ordinary rounding: 2e-7.  GH: groups of 16 ranks of
-// an epilogue thread (the eight warps halve the ranks).
+// accumulator is added to registers with ordinary rounding: 2e-7.  GH: groups of
+// 16 ranks of an epilogue thread (the eight warps halve the ranks).
 template <int GH>
 __global__ void __launch_bounds__(kLmThreads, 1) lora_shrink_kernel(const __grid_constant__ CUtensorMap amap,
                                                                  const LmArgs a) {
