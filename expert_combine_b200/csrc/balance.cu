@@ -897,7 +897,8 @@ __global__ void __launch_bounds__((kBalGradWarps + kBalGateWarps) * 32, 1) gate_
             __syncwarp();
         }
         float2 S2 = make_float2(0.0f, 0.0f), G2 = S2;
-        if (BAL && in_seq) {
+        const bool dense = BAL && in_seq;
+        if (dense) {
             float2 sum = make_float2(0.0f, 0.0f), dot = sum;
             float big = 0.0f;
 #pragma unroll
@@ -935,8 +936,10 @@ __global__ void __launch_bounds__((kBalGradWarps + kBalGateWarps) * 32, 1) gate_
         }
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
-            const float2 lo = mul2(x[2 * v], S2), gl = add2(g[2 * v], G2);
-            const float2 hi = mul2(x[2 * v + 1], S2), gh = add2(g[2 * v + 1], G2);
+            const float2 lo = mul2(x[2 * v], S2), hi = mul2(x[2 * v + 1], S2);
+            // a row without a part in the loss takes none of its g, which may be infinite or NaN
+            const float2 none = make_float2(0.0f, 0.0f);
+            const float2 gl = dense ? add2(g[2 * v], G2) : none, gh = dense ? add2(g[2 * v + 1], G2) : none;
             if constexpr (VEC) {
                 const int e = bal_expert<NV, VEC>(tm.wt, lane, 4 * v);
                 if (e < a.E) {

@@ -309,3 +309,26 @@ def test_the_gate_and_its_training_together(cuda_dev):
     # the weights that the gradient is taken of are the gate's
     sj = 1 / (1 + np.exp(-np.take_along_axis(x.astype(np.float64), np.maximum(ids.cpu().numpy(), 0), 1)))
     assert np.allclose(w.cpu().numpy()[mask != 0], (sj / sj.sum(1, keepdims=True))[mask != 0], rtol=1e-6)
+
+
+@pytest.mark.parametrize("grad_loss", [float("inf"), float("-inf"), float("nan")])
+@pytest.mark.parametrize("T,E,k", [(60, 40, 4), (60, 37, 4), (70, 512, 22), (60, 2560, 8)])
+def test_overflowed_loss_gradient_stays_in_its_sequences(cuda_dev, grad_loss, T, E, k):
+    """Rows of invalid tokens stay zero and rows of no sequence keep the gate's part alone."""
+    x, ids, mask, dw = _inputs(T, E, k, seed=6)
+    off = [7, 30, 30, 45]
+    tx, ti, tm, tw, to = _dev(cuda_dev, x, ids, mask, dw, np.asarray(off, np.int32))
+    _, counts, _, n = eb.moe_balance_loss(tx, ti, tm, 0.1, seq_offsets=to)
+    gl = torch.tensor([grad_loss], device=cuda_dev)
+    rest = dict(grad_loss=gl, coeff=0.1, counts=counts, seq_tokens=n, seq_offsets=to)
+    both = eb.moe_route_backward(tx, ti, tm, grad_weights=tw, **rest)
+    bal = eb.moe_route_backward(tx, ti, tm, **rest)
+    gate = eb.moe_route_backward(tx, ti, tm, grad_weights=tw)
+    torch.cuda.synchronize()
+    t = torch.arange(T, device=cuda_dev)
+    inside = (tm != 0) & (t >= off[0]) & (t < off[-1])
+    assert not both[tm == 0].any() and not bal[~inside].any()
+    assert torch.equal(both[~inside], gate[~inside])
+    # counts of 0 beside others: inf * 0 in the row's mean, so the formula is NaN all over the row
+    assert bool((counts == 0).any(1)[n > 0].all())
+    assert bool(both[inside].isnan().all()) and bool(bal[inside].isnan().all())
