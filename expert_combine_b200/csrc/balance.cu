@@ -165,10 +165,12 @@ __device__ __forceinline__ float2 sigmoid2(float2 x, float2& e, float& big) {
 
 // For any row: sigmoid(x) / exp(min(m, 0)) with m the row's largest logit, and
 // that times 1 - sigmoid(x).  With u = exp(-|x|), r = 1 / (1 + u) the sigmoid is
-// exp(min(x, 0)) r and 1 - sigmoid u r or r by the sign of x.  A row of -inf: 0.
+// exp(min(x, 0)) r and 1 - sigmoid u r or r by the sign of x.  A logit of -inf
+// gives 0, also in a row of nothing else; NaN gives NaN whatever m is (fmaxf
+// leaves NaN out of m, so a row of NaN and -inf has m = -inf).
 __device__ __forceinline__ float sigmoid_over(float x, float m, float& slope) {
     const float u = ex2_approx(fabsf(x) * -kLog2e), r = rcp_approx(1.0f + u);
-    const float s = m == -INFINITY ? 0.0f : ex2_approx((fminf(x, 0.0f) - fminf(m, 0.0f)) * kLog2e) * r;
+    const float s = x == -INFINITY ? 0.0f : ex2_approx((fminf(x, 0.0f) - fminf(m, 0.0f)) * kLog2e) * r;
     slope = s * (x >= 0.0f ? u * r : r);
     return s;
 }

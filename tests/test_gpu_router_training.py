@@ -332,3 +332,25 @@ def test_overflowed_loss_gradient_stays_in_its_sequences(cuda_dev, grad_loss, T,
     # counts of 0 beside others: inf * 0 in the row's mean, so the formula is NaN all over the row
     assert bool((counts == 0).any(1)[n > 0].all())
     assert bool(both[inside].isnan().all()) and bool(bal[inside].isnan().all())
+
+
+@pytest.mark.parametrize("T,E", [(30, 8), (30, 37), (30, 600), (4000, 256), (300, 2560), (200, 3001)])
+@pytest.mark.parametrize("kind", ["all", "beside -inf", "beside numbers"])
+def test_nan_logits_of_a_valid_token_reach_the_loss(cuda_dev, T, E, kind):
+    """A row of NaN is no row of -inf: its sequence's sums and the loss are NaN, another sequence's sums are not."""
+    x, ids, mask, dw = _inputs(T, E, 4, seed=3)
+    mask[[2, T - 1]] = 1
+    x[2], x[T - 1] = np.nan, 0.0
+    if kind == "beside -inf":
+        x[2, 1:] = -np.inf
+    if kind == "beside numbers":
+        x[2, 1:] = np.linspace(-3, 3, E - 1)
+    off = [0, T // 2, T]
+    tx, ti, tm, tw, to = _dev(cuda_dev, x, ids, mask, dw, np.asarray(off, np.int32))
+    loss, counts, probs, n = eb.moe_balance_loss(tx, ti, tm, 0.1, seq_offsets=to)
+    g = eb.moe_route_backward(tx, ti, tm, grad_loss=torch.ones(1, device=cuda_dev), coeff=0.1, counts=counts,
+                              seq_tokens=n, seq_offsets=to)
+    torch.cuda.synchronize()
+    assert bool(loss.isnan().all()) and bool(probs[0].isnan().all()) and bool(probs[1].isfinite().all())
+    rows = torch.arange(T, device=cuda_dev) != 2
+    assert bool(g[2].isnan().all()) and bool(g[rows].isfinite().all())
