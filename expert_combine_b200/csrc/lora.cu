@@ -34,9 +34,8 @@
 //     in 16-byte pieces.  A tile that several CTAs share is summed by the one
 //     that arrives last, from the partials, in the CTAs' order (an integer
 //     counter per tile; the sum's order does not depend on the arrival).  It
-//     writes v scaled and split into BF16 parts (3 for FP32 outputs: 2^-24 of v
-//     is left; 2 for BF16 outputs: 2^-16), in the layout of the next MMA's
-//     operand.
+//     writes v scaled and split into BF16 parts (3 for FP32 outputs: v whole; 2 for
+//     BF16 outputs: 2^-16 of v is left), in the layout of the next MMA's operand.
 //   expand  Work items are a tile x 128 columns, cut the same way.  D = sum over
 //     the parts v_p B^T; base arrives in the swizzled layout in which an epilogue
 //     thread reads its row without bank conflicts, the sum replaces it there,
@@ -526,6 +525,20 @@ __device__ __forceinline__ void lm_drain(uint64_t* full, int n, int issued) {
         mbar_wait_bounded(&full[j % n], static_cast<uint32_t>((j / n) & 1), kLmTimeout);
 }
 
+// The next part of v, which is left without it: the BF16 value next to v on the
+// side of zero, v itself excluded.  So no part of a v other than 0 is 0 or has
+// the other sign (down to where BF16 ends, 2^-133), and where B is infinite the
+// parts' products add up to v's own infinity, not to NaN; nor does a v above the
+// largest BF16 become infinite.  What is left is exact and at most one step of
+// the part, 2^-7 of v: after two parts a third takes it whole.  An infinite v
+// leaves infinity to the last part, NaN stays NaN.
+__device__ __forceinline__ float lm_part(float& v) {
+    const uint32_t bits = __float_as_uint(v);
+    const float p = v == 0.0f ? 0.0f : __uint_as_float((bits - 1u) & 0xffff0000u);
+    v -= p;
+    return p;
+}
+
 // v of 16 ranks from group gi of one row: scaled, split, written as operand rows.
 __device__ __forceinline__ void lm_write_v(const LmArgs& a, int tile, int gi, int row, float scale, float (&v)[16]) {
 #pragma unroll
@@ -533,13 +546,9 @@ __device__ __forceinline__ void lm_write_v(const LmArgs& a, int tile, int gi, in
     for (int p = 0; p < a.parts; ++p) {
         uint32_t w[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            w[i] = pack_bf16x2_rn(make_float2(v[2 * i], v[2 * i + 1]));
-            const float2 b = unpack_bf16x2(w[i]);
-            // the rest is exact; behind an infinity or NaN nothing is left
-            v[2 * i] = fabsf(b.x) < INFINITY ? v[2 * i] - b.x : 0.0f;
-            v[2 * i + 1] = fabsf(b.y) < INFINITY ? v[2 * i + 1] - b.y : 0.0f;
-        }
+        for (int i = 0; i < 8; ++i)
+            w[i] = p == a.parts - 1 ? pack_bf16x2_rn(make_float2(v[2 * i], v[2 * i + 1]))
+                                    : pack_bf16x2_rn(make_float2(lm_part(v[2 * i]), lm_part(v[2 * i + 1])));
         uint16_t* dst = a.v + (((static_cast<size_t>(tile) * a.parts + p) * a.ks + gi / 4) * kLmTile + row) * kLmSlab +
                         gi % 4 * 16;
         st_v4(dst, make_uint4(w[0], w[1], w[2], w[3]));
@@ -912,7 +921,9 @@ __global__ void __launch_bounds__(kLmThreads, 1) lora_expand_kernel(const __grid
                     tc_fence_after();
                     const uint32_t sbs = smem_addr(sb) + rb.slot * kLmSlabBytes;
                     const int steps = (min(a.R - s * kLmSlab, kLmSlab) + 15) / 16;
-                    for (int p = 0; p < a.parts; ++p)
+                    // the small parts first: every step cuts off what the sum so far cannot hold, always towards
+                    // zero, and the parts of a v have its sign
+                    for (int p = a.parts - 1; p >= 0; --p)
                         for (int k = 0; k < steps; ++k) {
                             mma_bf16(tmem + b * kLmCols, smem_desc_sw128(v + (p * a.ks + s) * kLmSlabBytes + 32u * k),
                                      smem_desc_sw128(sbs + 32u * k), idesc, more);

@@ -363,8 +363,9 @@ int router_logits(const uint16_t* x, int T, int H, const uint16_t* w3, int E, fl
  * v and the sums over r are FP32 (products of BF16 values are exact in FP32),
  * out is rounded once.  For batches that need a workspace (T > 256, or T > 192
  * with R > 32) the second product takes scales[a] * v in BF16 parts: three for
- * an FP32 out (2^-24 of v is left out), two for a BF16 out (2^-16).  No
- * floating-point atomics: results are the same run to run.
+ * an FP32 out (v whole), two for a BF16 out (2^-16 of v is left out).  Infinite
+ * values and NaN of x, A, B and scales give what the formula gives, for any T.
+ * No floating-point atomics: results are the same run to run.
  * Supported: H % 8 == 0, 8 <= H <= 65536, N % 8 == 0, 8 <= N <= 262144,
  * R % 8 == 0, 8 <= R <= 128, 1 <= L <= 4096, L * N < 2^31, T <= 2^24.
  */

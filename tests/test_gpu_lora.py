@@ -237,3 +237,54 @@ def test_refusals(cuda_dev):
                     workspace=torch.empty(16, dtype=torch.uint8, device=cuda_dev))
     with pytest.raises(eb.MoEBoundaryError, match="needs H, N and R"):
         call(a=i["a"][:, :4].contiguous(), b=i["b"][:, :, :4].contiguous())
+
+
+def _same_class(got, want):
+    """NaN where the definition is NaN, an infinity of the definition's sign where it is infinite, else finite."""
+    return bool((got.isnan() == want.isnan()).all()) and bool((got.isposinf() == want.isposinf()).all()) and \
+        bool((got.isneginf() == want.isneginf()).all())
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("T,N,R", [(40, 136, 24), (400, 136, 24), (400, 264, 64), (900, 128, 128)])
+def test_infinite_values_of_the_second_factor(cuda_dev, T, N, R, bf16):
+    """v * inf is an infinity of v's sign, inf - inf and 0 * inf NaN, for few and for many tokens."""
+    H, L = 256, 4
+    i = _inputs(cuda_dev, T, H, N, R, L, bf16, seed=17)
+    inf = float("inf")
+    i["b"][1, 5, 3] = inf
+    i["b"][1, N - 1, R - 1] = -inf
+    i["b"][2, 7, 0], i["b"][2, 7, 1] = inf, -inf
+    i["b"][2, 9, 2] = float("nan")
+    i["x"][T // 2] = 0.0
+    i["x"][T // 3, 10] = inf
+    t = torch.nonzero(i["adapter_ids"] >= 0).flatten()
+    v = torch.einsum("th,trh->tr", i["x"][t].double(), i["a"][i["adapter_ids"][t].long()].double())
+    some = v[v.isfinite() & (v != 0)].abs()
+    assert float(some.min()) > 1e-5          # the signs of v are the definition's
+    want, tol = _reference(i)
+    got = eb.lora_add(i["base"], i["x"], i["a"], i["b"], i["adapter_ids"], scales=i["scales"])
+    torch.cuda.synchronize()
+    assert _same_class(got, want) and bool(want.isinf().any()) and bool(want.isnan().any())
+    ok = want.isfinite()
+    assert bool(((got.double() - want).abs() <= tol)[ok].all())
+    assert eb.device_status() == 0
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("T", [20, 300])
+def test_first_products_above_the_largest_bf16(cuda_dev, T, bf16):
+    """v between the largest BF16 and the largest FP32 value is no infinity."""
+    H, N, R = 64, 16, 8
+    i = _inputs(cuda_dev, T, H, N, R, 1, bf16, seed=2, ids=[0] * T)
+    for n in ("x", "a", "b"):
+        i[n].zero_()
+    top = torch.finfo(torch.bfloat16).max
+    i["scales"] = None
+    i["a"][0, 0, 0] = i["a"][0, 0, 1] = i["a"][0, 1, 2] = i["a"][0, 1, 3] = 1.0
+    i["x"][:, 0], i["x"][:, 1], i["x"][:, 2], i["x"][:, 3] = top, 1.5 * 2.0 ** 119, -top, -1.5 * 2.0 ** 119
+    i["b"][0, 0, 0], i["b"][0, 1, 1], i["b"][0, 2, 0] = 2.0 ** -100, 2.0 ** -100, 0.5
+    want, tol = _reference(i)
+    got = eb.lora_add(i["base"], i["x"], i["a"], i["b"], i["adapter_ids"])
+    torch.cuda.synchronize()
+    assert bool(got.isfinite().all()) and bool(((got.double() - want).abs() <= tol).all())
