@@ -2,6 +2,7 @@
 from __future__ import annotations
 
 import ctypes
+import inspect
 import os
 import threading
 from typing import Optional
@@ -36,15 +37,36 @@ def tracing() -> bool:
     return _trace_depth > 0
 
 
-def _traced(fn):
+def _beside(stream, fn, args, kwargs):
+    """A call on the caller's ``stream``, which is the current one meanwhile: what
+    the call allocates is then that stream's memory.  A block of the caller's
+    own current stream could still be in use there, and a workspace, dropped on
+    return, could be handed out there again while the kernels run.  The outputs
+    are marked as used on the caller's current stream too."""
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream.cuda_stream)
+    before = torch.cuda.current_stream(stream.device)
+    with torch.cuda.stream(stream):
+        result = fn(*args, **kwargs)
+    if before != stream:
+        for t in result if isinstance(result, (tuple, list)) else (result,):
+            if isinstance(t, torch.Tensor):
+                t.record_stream(before)
+    return result
+
+
+def _entry(fn):
+    """A public call: its NVTX range, and its ``stream`` argument (the last)."""
     name = fn.__name__
+    place = list(inspect.signature(fn).parameters).index("stream")
 
     def wrapper(*args, **kwargs):
+        stream = kwargs.get("stream") if len(args) <= place else args[place]
         if _trace_depth <= 0:
-            return fn(*args, **kwargs)
+            return fn(*args, **kwargs) if stream is None else _beside(stream, fn, args, kwargs)
         torch.cuda.nvtx.range_push(name)
         try:
-            return fn(*args, **kwargs)
+            return fn(*args, **kwargs) if stream is None else _beside(stream, fn, args, kwargs)
         finally:
             torch.cuda.nvtx.range_pop()
 
@@ -53,6 +75,7 @@ def _traced(fn):
     wrapper.__doc__ = fn.__doc__
     wrapper.__wrapped__ = fn
     return wrapper
+
 
 STAGE_ROUTE = 0
 STAGE_NORM_QUANT = 1
@@ -226,7 +249,7 @@ def device_status() -> int:
     return v
 
 
-@_traced
+@_entry
 def moe_route(logits: torch.Tensor, bias: torch.Tensor, token_mask: torch.Tensor, k: int,
               topk_ids: Optional[torch.Tensor] = None, topk_weights: Optional[torch.Tensor] = None,
               stream=None):
@@ -249,7 +272,7 @@ def moe_route(logits: torch.Tensor, bias: torch.Tensor, token_mask: torch.Tensor
     return topk_ids, topk_weights
 
 
-@_traced
+@_entry
 def moe_route_check_fast_sigmoid(stream=None) -> float:
     """Largest |fast - exact| sigmoid over every binary32 input, measured on the
     device (the bound moe_route's shortlist relies on); synchronises."""
@@ -264,7 +287,7 @@ def moe_route_check_fast_sigmoid(stream=None) -> float:
 ROUTE_FAST_SIGMOID_BOUND = 2.0 ** -21
 
 
-@_traced
+@_entry
 def norm_quant_nvfp4(x: torch.Tensor, num_tokens: int, norm_w: torch.Tensor, gain_center: float,
                      eps: float, global_scale: torch.Tensor, tp: int = 1,
                      packed: Optional[torch.Tensor] = None, sf: Optional[torch.Tensor] = None,
@@ -295,7 +318,7 @@ def norm_quant_nvfp4(x: torch.Tensor, num_tokens: int, norm_w: torch.Tensor, gai
     return packed, sf
 
 
-@_traced
+@_entry
 def moe_route_norm_quant(logits: torch.Tensor, bias: torch.Tensor, token_mask: torch.Tensor, k: int,
                          x: torch.Tensor, norm_w: torch.Tensor, gain_center: float, eps: float,
                          global_scale: torch.Tensor, tp: int = 1,
@@ -343,7 +366,7 @@ def route_norm_quant_kernels(M: int, H: int, E: int, k: int, tp: int = 1) -> int
     device (for a 16-byte-aligned x); -1 when unsupported or without a device."""
     return int(load().moe_route_norm_quant_kernels(M, H, tp, E, k))
 
-@_traced
+@_entry
 def expert_combine(expert_out: torch.Tensor, num_rows: int, row_idx: torch.Tensor,
                    weights: torch.Tensor, norm_w: torch.Tensor, gain_center: float, eps: float,
                    out: Optional[torch.Tensor] = None, stream=None):
@@ -366,7 +389,7 @@ def expert_combine(expert_out: torch.Tensor, num_rows: int, row_idx: torch.Tenso
     return out
 
 
-@_traced
+@_entry
 def residual_join(residual: torch.Tensor, branch: torch.Tensor, gain: torch.Tensor, alpha: float,
                   beta: float, eps: float, next_w: Optional[torch.Tensor] = None,
                   next_gc: float = 1.0, next_eps: float = 1e-6,
@@ -390,7 +413,7 @@ def residual_join(residual: torch.Tensor, branch: torch.Tensor, gain: torch.Tens
     return next_prenorm
 
 
-@_traced
+@_entry
 def expert_combine_join(expert_out: torch.Tensor, num_rows: int, row_idx: torch.Tensor,
                         weights: torch.Tensor, norm_w: torch.Tensor, gain_center: float,
                         eps: float, residual: torch.Tensor, gain: torch.Tensor, alpha: float,
@@ -430,7 +453,7 @@ def dispatch_workspace_size(T: int, k: int, E: int) -> int:
     return int(load().moe_dispatch_workspace_size(T, k, E))
 
 
-@_traced
+@_entry
 def moe_dispatch(topk_ids: torch.Tensor, num_experts: int, expert_begin: int = 0,
                  expert_offsets: Optional[torch.Tensor] = None, row_idx: Optional[torch.Tensor] = None,
                  row_token: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
@@ -468,7 +491,7 @@ def moe_dispatch(topk_ids: torch.Tensor, num_experts: int, expert_begin: int = 0
     return expert_offsets, row_idx, row_token
 
 
-@_traced
+@_entry
 def moe_dispatch_noalloc(topk_ids: torch.Tensor, num_experts: int, expert_begin: int = 0,
                          expert_offsets: Optional[torch.Tensor] = None,
                          row_idx: Optional[torch.Tensor] = None,
@@ -519,7 +542,7 @@ def _router_batch(fn, logits, topk_ids, token_mask, seq_offsets):
     return T, E, k, Q, dev, at
 
 
-@_traced
+@_entry
 def moe_balance_loss(logits: torch.Tensor, topk_ids: torch.Tensor, token_mask: torch.Tensor, coeff: float,
                      seq_offsets: Optional[torch.Tensor] = None, loss: Optional[torch.Tensor] = None,
                      counts: Optional[torch.Tensor] = None, prob_sums: Optional[torch.Tensor] = None,
@@ -560,7 +583,7 @@ def moe_balance_loss(logits: torch.Tensor, topk_ids: torch.Tensor, token_mask: t
     return loss, counts, prob_sums, seq_tokens
 
 
-@_traced
+@_entry
 def moe_route_backward(logits: torch.Tensor, topk_ids: torch.Tensor, token_mask: torch.Tensor,
                        grad_weights: Optional[torch.Tensor] = None, grad_loss: Optional[torch.Tensor] = None,
                        coeff: float = 0.0, counts: Optional[torch.Tensor] = None,
@@ -591,7 +614,7 @@ def moe_route_backward(logits: torch.Tensor, topk_ids: torch.Tensor, token_mask:
     return grad_logits
 
 
-@_traced
+@_entry
 def router_weight_prepare(w: torch.Tensor, w3: Optional[torch.Tensor] = None, stream=None):
     """FP32 router weight [E, H] -> its three BF16 parts [3, E, H] (done once)."""
     _want(w, torch.float32, "w")
@@ -605,7 +628,7 @@ def router_weight_prepare(w: torch.Tensor, w3: Optional[torch.Tensor] = None, st
     return w3
 
 
-@_traced
+@_entry
 def router_logits(x: torch.Tensor, w3: torch.Tensor, scale: float = 1.0,
                   logits: Optional[torch.Tensor] = None, stream=None):
     """Router projection on the tensor cores: logits float32 [T, E] =
@@ -631,7 +654,7 @@ def lora_workspace_size(T: int, H: int, N: int, R: int, L: int) -> int:
     return int(load().lora_workspace_size(T, H, N, R, L))
 
 
-@_traced
+@_entry
 def lora_add(base: torch.Tensor, x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, adapter_ids: torch.Tensor,
              scales: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
              workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
@@ -675,7 +698,7 @@ def finalize_ar_workspace_size(world: int, T_max: int, H: int) -> int:
     return int(load().finalize_ar_workspace_size(world, T_max, H))
 
 
-@_traced
+@_entry
 def finalize_ar_workspace_init(workspace, world: int, T_max: int, H: int, stream=None) -> None:
     """Zero a workspace's call counter and flags (a tensor or a device address)."""
     ptr = _ptr(workspace) if isinstance(workspace, torch.Tensor) else ctypes.c_void_p(int(workspace))
@@ -698,7 +721,7 @@ def _far_rank_check(fn, expert_out, row_idx, weights, norm_w, out):
         raise ValueError(f"{fn}: shape mismatch")
 
 
-@_traced
+@_entry
 def expert_finalize_allreduce(expert_out: torch.Tensor, num_rows: int, row_idx: torch.Tensor,
                               weights: torch.Tensor, norm_w: torch.Tensor, gain_center: float, eps: float,
                               workspaces, rank: int, T_max: int, out: Optional[torch.Tensor] = None,
@@ -725,7 +748,7 @@ def expert_finalize_allreduce(expert_out: torch.Tensor, num_rows: int, row_idx: 
     return out
 
 
-@_traced
+@_entry
 def expert_finalize_allreduce_local(expert_outs, num_rows, row_idx, weights, norm_w: torch.Tensor,
                                     gain_center: float, eps: float, workspaces, T_max: int, outs=None,
                                     stream=None):
