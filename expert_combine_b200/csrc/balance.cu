@@ -313,8 +313,12 @@ struct RowFeed {
     // The next row.
     __device__ __forceinline__ void take(float2 (&x)[2 * NV]) {
         if constexpr (VEC) {
-            // after a wait that ran out the values are not the row's, but the team keeps its barriers
-            if (flying > 0 && !dead) dead = !mbar_wait_bounded(&full[slot], static_cast<uint32_t>(phase), kBalTimeout);
+            // After a wait that ran out the values are not the row's, but the team keeps its barriers.  Every lane
+            // polls, and the warp takes it for run out together where it ran out in one of them, so that the
+            // lanes go on agreeing about what is in flight.
+            if (flying > 0 && !dead)
+                dead = __any_sync(0xffffffffu,
+                                  !mbar_wait_bounded(&full[slot], static_cast<uint32_t>(phase), kBalTimeout));
             const float* p = slots + slot * NV * 128 + 4 * lane;
 #pragma unroll
             for (int v = 0; v < NV; ++v) {
