@@ -464,7 +464,10 @@ int moe_route_backward(const float* logits, const int32_t* topk_ids, const uint8
     const size_t rows = static_cast<size_t>(T) * E * 4, picks = static_cast<size_t>(T) * k * 4;
     if (overlap(grad_logits, rows, logits, rows) || overlap(grad_logits, rows, topk_ids, picks) ||
         overlap(grad_logits, rows, grad_weights, picks) || overlap(grad_logits, rows, token_mask, static_cast<size_t>(T)) ||
-        overlap(grad_logits, rows, counts, static_cast<size_t>(Q) * E * 4))
+        overlap(grad_logits, rows, counts, static_cast<size_t>(Q) * E * 4) ||
+        overlap(grad_logits, rows, seq_tokens, static_cast<size_t>(Q) * 4) ||
+        overlap(grad_logits, rows, seq_offsets, (static_cast<size_t>(Q) + 1) * 4) ||
+        overlap(grad_logits, rows, grad_loss, 4))
         return fail(MB_ERR_INVALID_ARG, "%s: grad_logits overlaps an input", fn);
     const GateGradLaunch b{logits, topk_ids, token_mask, T, E, k, grad_weights, grad_loss, coeff, counts, seq_tokens,
                            seq_offsets, Q, grad_logits};

@@ -101,3 +101,21 @@ def test_library_refuses_before_any_launch():
     assert back(Q=2) == 1 and back(E=4097) == 2 and back(T=-1) == 1 and back(k=17) == 2
     assert back(ptr=odd) == 1 and back(dw=odd) == 1 and back(out=odd) == 1
     assert eb.supported(eb.STAGE_BALANCE, 8192, 0, 256, 8, 4) and not eb.supported(eb.STAGE_BALANCE, 1, 0, 4, 8, 1)
+
+
+def test_gradient_over_any_input_is_refused():
+    """grad_logits may share no byte with what other CTAs still read."""
+    lib = eb.load()
+    T, E, k, Q = 4, 16, 2, 3
+    at = {n: (i + 1) << 32 for i, n in enumerate(("x", "ids", "mask", "dw", "dl", "counts", "n", "off"))}
+    size = {"x": T * E * 4, "ids": T * k * 4, "mask": T, "dw": T * k * 4, "dl": 4, "counts": Q * E * 4, "n": Q * 4,
+            "off": (Q + 1) * 4}
+    P = {n: ctypes.c_void_p(a) for n, a in at.items()}
+
+    def back(out):
+        return lib.moe_route_backward(P["x"], P["ids"], P["mask"], T, E, k, P["dw"], P["dl"], 0.1, P["counts"], P["n"],
+                                      P["off"], Q, ctypes.c_void_p(out), None)
+    for n in at:
+        last = (at[n] + size[n] - 1) & ~15
+        for out in (at[n], last, at[n] - T * E * 4 + 16):
+            assert back(out) == 1 and "overlaps" in eb.last_error(), n
