@@ -357,9 +357,9 @@ int moe_dispatch(const int32_t* topk_ids, int T, int k, int expert_begin, int E,
                        fn);
 }
 
-// Whether two ranges of memory share a byte (false for a null pointer).
+// Whether two ranges of memory share a byte (a null pointer shares none).
 static bool overlap(const void* p, size_t n, const void* q, size_t m) {
-    if (!p || !q) return false;
+    if (!p || !q || n == 0 || m == 0) return false;
     const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
     return a < b + m && b < a + n;
 }
@@ -440,6 +440,17 @@ int moe_balance_loss(const float* logits, const int32_t* topk_ids, const uint8_t
                         workspace ? workspace_bytes : static_cast<size_t>(0));
         if (!aligned16(workspace)) return fail(MB_ERR_INVALID_ARG, "%s: workspace must be 16-byte aligned", fn);
     }
+    const size_t t = static_cast<size_t>(T), q = static_cast<size_t>(Q);
+    const struct {
+        const void* p;
+        size_t bytes;
+    } parts[] = {{loss, 4},           {counts, q * E * 4},  {prob_sums, q * E * 4}, {seq_tokens, q * 4},
+                 {workspace, need},   {logits, t * E * 4},  {topk_ids, t * k * 4},  {token_mask, t},
+                 {seq_offsets, (q + 1) * 4}};
+    for (int i = 0; i < 5; ++i)          // what is written, against all behind it
+        for (int j = i + 1; j < 9; ++j)
+            if (overlap(parts[i].p, parts[i].bytes, parts[j].p, parts[j].bytes))
+                return fail(MB_ERR_INVALID_ARG, "%s: an output or the workspace overlaps another array", fn);
     const BalanceLaunch b{logits, topk_ids, token_mask, seq_offsets, T, E, k, Q, coeff, loss, counts, prob_sums,
                           seq_tokens, workspace};
     return cuda_status(launch_balance_loss(b, static_cast<cudaStream_t>(stream)), fn);

@@ -257,6 +257,7 @@ int expert_combine_join(const uint16_t* expert_out, int64_t num_rows, int H, con
  *               16-byte aligned (may be NULL when that size is 0: small
  *               batches); needs no initialisation; two calls that overlap on
  *               the GPU need two
+ * The outputs and the workspace lie apart from the inputs and from one another.
  * Sums are FP32 in an order fixed by the sizes (no floating-point atomics).
  * Offsets that are not ascending give undefined outputs, never an access out
  * of bounds.  T == 0 writes zeros (topk_ids, logits and token_mask may then be

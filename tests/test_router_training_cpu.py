@@ -119,3 +119,24 @@ def test_gradient_over_any_input_is_refused():
         last = (at[n] + size[n] - 1) & ~15
         for out in (at[n], last, at[n] - T * E * 4 + 16):
             assert back(out) == 1 and "overlaps" in eb.last_error(), n
+
+
+def test_loss_outputs_over_another_array_are_refused():
+    """Outputs and workspace may share no byte with an input or with one another."""
+    lib = eb.load()
+    T, E, k, Q = 100000, 16, 2, 3
+    need = eb.balance_workspace_size(T, E, Q)
+    assert need > 0
+    size = {"x": T * E * 4, "ids": T * k * 4, "mask": T, "off": (Q + 1) * 4, "loss": 4, "counts": Q * E * 4,
+            "probs": Q * E * 4, "n": Q * 4, "ws": need}
+    at = {n: (i + 1) << 32 for i, n in enumerate(size)}
+
+    def loss(**moved):
+        p = {n: ctypes.c_void_p(a) for n, a in {**at, **moved}.items()}
+        return lib.moe_balance_loss(p["x"], p["ids"], p["mask"], T, E, k, p["off"], Q, 0.1, p["loss"], p["counts"],
+                                    p["probs"], p["n"], p["ws"], ctypes.c_size_t(need), None)
+    for out in ("loss", "counts", "probs", "n", "ws"):
+        for other in size:
+            if other != out:
+                for where in (at[other], (at[other] + size[other] - 1) & ~15, at[other] - ((size[out] - 1) & ~15)):
+                    assert loss(**{out: where}) == 1 and "overlaps" in eb.last_error(), (out, other)
