@@ -397,8 +397,11 @@ int lora_add(const void* base, int base_bf16, const uint16_t* x, int T, int H, c
             return fail(MB_ERR_INVALID_ARG, "%s: needs a workspace of %zu bytes (got %zu)", fn, need,
                         workspace ? workspace_bytes : static_cast<size_t>(0));
         if (!aligned256(workspace)) return fail(MB_ERR_INVALID_ARG, "%s: workspace must be 256-byte aligned", fn);
-        if (overlap(workspace, need, out, nout) || overlap(workspace, need, base, nout))
-            return fail(MB_ERR_INVALID_ARG, "%s: workspace overlaps base or out", fn);
+        if (overlap(workspace, need, out, nout) || overlap(workspace, need, base, nout) ||
+            overlap(workspace, need, x, static_cast<size_t>(T) * H * 2) || overlap(workspace, need, a, l * H) ||
+            overlap(workspace, need, b, l * N) || overlap(workspace, need, adapter_ids, static_cast<size_t>(T) * 4) ||
+            overlap(workspace, need, scales, static_cast<size_t>(L) * 4))
+            return fail(MB_ERR_INVALID_ARG, "%s: workspace overlaps out or an input", fn);
     }
     const LoraLaunch ll{base, out, base_bf16 != 0, x, a, b, adapter_ids, scales, T, H, N, R, L, workspace};
     return cuda_status(launch_lora_add(ll, static_cast<cudaStream_t>(stream)), fn);

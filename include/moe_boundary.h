@@ -358,9 +358,9 @@ int router_logits(const uint16_t* x, int T, int H, const uint16_t* w3, int E, fl
  *   a  [L, R, H] BF16       b  [L, N, R] BF16
  *   adapter_ids  [T] int32  scales  [L] FP32, or NULL for 1
  *   workspace  device scratch of lora_workspace_size(T, H, N, R, L) bytes,
- *              256-byte aligned (may be NULL when that size is 0: few tokens);
- *              needs no initialisation; two calls that overlap on the GPU need
- *              two
+ *              256-byte aligned, apart from out and the inputs (may be NULL when
+ *              that size is 0: few tokens); needs no initialisation; two calls
+ *              that overlap on the GPU need two
  * v and the sums over r are FP32 (products of BF16 values are exact in FP32),
  * out is rounded once.  For batches that need a workspace (T > 256, or T > 192
  * with R > 32) the second product takes scales[a] * v in BF16 parts: three for

@@ -52,3 +52,19 @@ def test_library_refuses_before_any_launch():
     assert eb.lora_workspace_size(4, 64, 32, 9, 2) == 0
     assert eb.supported(eb.STAGE_LORA, 1, 8192, 256, 16, 8) and not eb.supported(eb.STAGE_LORA, 1, 8192, 256, 256, 8)
     assert not eb.supported(eb.STAGE_LORA, 1, 64, 262144, 8, 4097)
+
+
+def test_workspace_over_any_array_is_refused():
+    """The plan and the partial sums of a batch may share no byte with what the call reads."""
+    lib = eb.load()
+    T, H, N, R, L = 300, 64, 32, 8, 2
+    need = eb.lora_workspace_size(T, H, N, R, L)
+    size = {"base": T * N * 4, "x": T * H * 2, "a": L * R * H * 2, "b": L * N * R * 2, "ids": T * 4, "scales": L * 4,
+            "out": T * N * 4}
+    at = {n: (i + 1) << 32 for i, n in enumerate(size)}
+    P = {n: ctypes.c_void_p(a) for n, a in at.items()}
+    for n in size:
+        for ws in (at[n], (at[n] + size[n] - 1) & ~255, at[n] - ((need - 1) & ~255)):
+            assert lib.lora_add(P["base"], 0, P["x"], T, H, P["a"], P["b"], N, R, L, P["ids"], P["scales"], P["out"],
+                                ctypes.c_void_p(ws), ctypes.c_size_t(need), None) == 1, n
+            assert "workspace overlaps" in eb.last_error(), n
