@@ -586,12 +586,12 @@ def moe_balance_loss(logits: torch.Tensor, topk_ids: torch.Tensor, token_mask: t
 @_entry
 def moe_route_backward(logits: torch.Tensor, topk_ids: torch.Tensor, token_mask: torch.Tensor,
                        grad_weights: Optional[torch.Tensor] = None, grad_loss: Optional[torch.Tensor] = None,
-                       coeff: float = 0.0, counts: Optional[torch.Tensor] = None,
+                       coeff: Optional[float] = None, counts: Optional[torch.Tensor] = None,
                        seq_tokens: Optional[torch.Tensor] = None, seq_offsets: Optional[torch.Tensor] = None,
                        grad_logits: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """Gradient of the router's logits (float32 [T, E]) from ``grad_weights``
     (of moe_route's weights, float32 [T, k]), from ``grad_loss`` (of
-    moe_balance_loss's loss, float32 [1]; with that call's coeff, counts,
+    moe_balance_loss's loss, float32 [1]; needs that call's coeff, counts,
     seq_tokens and seq_offsets), or from both."""
     fn = "moe_route_backward"
     T, E, k, Q, dev, (at_logits, at_ids, at_mask, at_offsets) = _router_batch(fn, logits, topk_ids, token_mask,
@@ -599,8 +599,8 @@ def moe_route_backward(logits: torch.Tensor, topk_ids: torch.Tensor, token_mask:
     if grad_weights is not None and grad_weights.shape != (T, k):
         raise ValueError(f"{fn}: shape mismatch")
     if grad_loss is not None:
-        if counts is None or seq_tokens is None:
-            raise ValueError(f"{fn}: grad_loss needs counts and seq_tokens")
+        if coeff is None or counts is None or seq_tokens is None:
+            raise ValueError(f"{fn}: grad_loss needs coeff, counts and seq_tokens")
         if grad_loss.numel() != 1 or counts.shape != (Q, E) or seq_tokens.numel() != Q:
             raise ValueError(f"{fn}: shape mismatch")
     if grad_logits is None:
@@ -609,8 +609,9 @@ def moe_route_backward(logits: torch.Tensor, topk_ids: torch.Tensor, token_mask:
         raise ValueError(f"{fn}: shape mismatch")
     _enqueue(fn, dev, stream, at_logits, at_ids, at_mask, T, E, k,
              _take(grad_weights, torch.float32, dev, "grad_weights"), _take(grad_loss, torch.float32, dev, "grad_loss"),
-             coeff, _take(counts, torch.int32, dev, "counts"), _take(seq_tokens, torch.int32, dev, "seq_tokens"),
-             at_offsets, Q, _take(grad_logits, torch.float32, dev, "grad_logits"))
+             0.0 if coeff is None else coeff, _take(counts, torch.int32, dev, "counts"),
+             _take(seq_tokens, torch.int32, dev, "seq_tokens"), at_offsets, Q,
+             _take(grad_logits, torch.float32, dev, "grad_logits"))
     return grad_logits
 
 

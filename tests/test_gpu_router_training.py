@@ -354,3 +354,16 @@ def test_nan_logits_of_a_valid_token_reach_the_loss(cuda_dev, T, E, kind):
     assert bool(loss.isnan().all()) and bool(probs[0].isnan().all()) and bool(probs[1].isfinite().all())
     rows = torch.arange(T, device=cuda_dev) != 2
     assert bool(g[2].isnan().all()) and bool(g[rows].isfinite().all())
+
+
+def test_loss_gradient_without_its_coefficient_is_refused(cuda_dev):
+    """Not a silent gradient of zero: grad_loss comes with the loss call's coeff, counts and seq_tokens."""
+    x, ids, mask, dw = _inputs(20, 16, 2, seed=1)
+    tx, ti, tm, tw = _dev(cuda_dev, x, ids, mask, dw)
+    _, counts, _, n = eb.moe_balance_loss(tx, ti, tm, 0.1)
+    good = dict(grad_loss=torch.ones(1, device=cuda_dev), coeff=0.1, counts=counts, seq_tokens=n)
+    assert eb.moe_route_backward(tx, ti, tm, **good).any()
+    for name in ("coeff", "counts", "seq_tokens"):
+        with pytest.raises(ValueError, match="grad_loss needs"):
+            eb.moe_route_backward(tx, ti, tm, **{k: v for k, v in good.items() if k != name})
+    eb.moe_route_backward(tx, ti, tm, grad_weights=tw)         # the gate alone needs none
