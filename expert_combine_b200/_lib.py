@@ -553,8 +553,16 @@ def moe_balance_loss(logits: torch.Tensor, topk_ids: torch.Tensor, token_mask: t
     ``seq_offsets`` (int32 [Q + 1] on the device, ascending) cuts the tokens
     into the sequences the loss is averaged over; without it the batch is one.
     ``workspace`` is a uint8 CUDA tensor of at least ``balance_workspace_size``
-    bytes (0 for small batches); when omitted, one is allocated here."""
+    bytes (0 for small batches); when omitted, one is allocated here.
+
+    The loss has no autograd history: its gradient comes from
+    moe_route_backward.  So that it is not lost unnoticed, ``logits`` that
+    require a gradient are refused while gradients are recorded; pass
+    ``logits.detach()``."""
     fn = "moe_balance_loss"
+    if logits.requires_grad and torch.is_grad_enabled():
+        raise ValueError(f"{fn}: logits require a gradient, which this call does not record; pass logits.detach() and "
+                         "take the gradient from moe_route_backward")
     T, E, k, Q, dev, (at_logits, at_ids, at_mask, at_offsets) = _router_batch(fn, logits, topk_ids, token_mask,
                                                                               seq_offsets)
     where = logits.device
@@ -666,7 +674,8 @@ def lora_add(base: torch.Tensor, x: torch.Tensor, a: torch.Tensor, b: torch.Tens
     base and out are float32 or bfloat16, x [T, H], a [L, R, H] and b [L, N, R]
     bfloat16.  ``out=base`` works in place; without ``out`` a tensor is
     allocated, and so is ``workspace`` (uint8, ``lora_workspace_size`` bytes, 0
-    for few tokens)."""
+    for few tokens).  A serving call: it has no backward pass and records no
+    gradient."""
     fn = "lora_add"
     bf16 = base.dtype is torch.bfloat16
     dtype = torch.bfloat16 if bf16 else torch.float32

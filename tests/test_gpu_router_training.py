@@ -367,3 +367,29 @@ def test_loss_gradient_without_its_coefficient_is_refused(cuda_dev):
         with pytest.raises(ValueError, match="grad_loss needs"):
             eb.moe_route_backward(tx, ti, tm, **{k: v for k, v in good.items() if k != name})
     eb.moe_route_backward(tx, ti, tm, grad_weights=tw)         # the gate alone needs none
+
+
+def test_inside_an_autograd_function(cuda_dev):
+    """The loss and its gradient as one node of a caller's graph: the parameters below it get the formula's gradient."""
+    class Balance(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, logits, ids, mask):
+            loss, counts, _, n = eb.moe_balance_loss(logits, ids, mask, 0.5)
+            ctx.save_for_backward(logits, ids, mask, counts, n)
+            return loss
+
+        @staticmethod
+        def backward(ctx, g):
+            logits, ids, mask, counts, n = ctx.saved_tensors
+            return eb.moe_route_backward(logits, ids, mask, grad_loss=g, coeff=0.5, counts=counts, seq_tokens=n), None, None
+
+    x, ids, mask, _ = _inputs(40, 24, 3, seed=2, masked=0.1)
+    x = np.where(mask[:, None] != 0, x, 0).astype(np.float32)
+    tx, ti, tm = _dev(cuda_dev, x, ids, mask)
+    tx.requires_grad_()
+    with pytest.raises(ValueError, match="require a gradient"):
+        eb.moe_balance_loss(tx, ti, tm, 0.5)
+    (3.0 * Balance.apply(tx, ti, tm)).sum().backward()
+    _, counts, _, n = balance(x, ids, mask, 0.5)
+    want, mag = backward(x, ids, mask, grad_loss=3.0, coeff=0.5, counts=counts, seq_tokens=n)
+    assert np.all(np.abs(tx.grad.cpu().numpy() - want) <= (2 * (_xmax(x) + 40) + 60) * U * mag + 1e-37)

@@ -140,3 +140,17 @@ def test_loss_outputs_over_another_array_are_refused():
             if other != out:
                 for where in (at[other], (at[other] + size[other] - 1) & ~15, at[other] - ((size[out] - 1) & ~15)):
                     assert loss(**{out: where}) == 1 and "overlaps" in eb.last_error(), (out, other)
+
+
+def test_a_loss_that_would_lose_its_gradient_is_refused():
+    """logits that require a gradient, while gradients are recorded; detached or without recording they go on."""
+    T, E, k = 4, 16, 2
+    x = torch.zeros(T, E, requires_grad=True)
+    rest = (torch.zeros(T, k, dtype=I32), torch.ones(T, dtype=U8), 0.1)
+    for logits in (x, x * 2):
+        with pytest.raises(ValueError, match="moe_route_backward"):
+            eb.moe_balance_loss(logits, *rest)
+    with pytest.raises(ValueError, match="CUDA tensor"):
+        eb.moe_balance_loss(x.detach(), *rest)
+    with torch.no_grad(), pytest.raises(ValueError, match="CUDA tensor"):
+        eb.moe_balance_loss(x, *rest)
