@@ -10,7 +10,7 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libmoe_boundary.so")
 SOURCES = ["moe_boundary.cu", "api.cu", "combine.cu", "norm_quant.cu", "route.cu", "decode.cu", "router_proj.cu", "dispatch.cu",
            "dispatch_noalloc.cu", "finalize_ar.cu", "balance.cu", "lora.cu",
-           "common.cuh", "ring.cuh", "route.cuh", "tmem.cuh", "internal.h", "tmap.h"]
+           "common.cuh", "ring.cuh", "route.cuh", "tmem.cuh", "mma.cuh", "internal.h", "tmap.h"]
 HEADER = os.path.join(os.path.dirname(HERE), "include", "moe_boundary.h")
 
 NVCC_FLAGS = [

@@ -110,18 +110,6 @@ __device__ __forceinline__ void named_bar_sync(int id, int count) {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(count) : "memory");
 }
 
-// The same barrier; true when `p` was true in every thread.
-__device__ __forceinline__ bool named_bar_and(int id, int count, bool p) {
-    int r;
-    asm volatile(
-        "{\n\t.reg .pred a, b;\n\tsetp.ne.s32 a, %3, 0;\n\tbar.red.and.pred b, %1, %2, a;\n\t"
-        "selp.s32 %0, 1, 0, b;\n\t}"
-        : "=r"(r)
-        : "r"(id), "r"(count), "r"(static_cast<int>(p))
-        : "memory");
-    return r != 0;
-}
-
 // ------------------------------------------------------------------ loads
 __device__ __forceinline__ uint4 ld_nc_v4(const void* p) {
     uint4 v;
@@ -309,11 +297,6 @@ __device__ __forceinline__ uint4 lds128(uint32_t addr) {
                  : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                  : "r"(addr));
     return v;
-}
-
-__device__ __forceinline__ void sts128(uint32_t addr, uint4 v) {
-    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
-                 : "memory");
 }
 
 // 2-D tiled TMA load global -> shared (no multicast), completing on an mbarrier.

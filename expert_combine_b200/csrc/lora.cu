@@ -46,7 +46,7 @@
 #include "internal.h"
 #include "common.cuh"
 #include "tmap.h"
-#include "tmem.cuh"
+#include "mma.cuh"
 
 namespace mb {
 

@@ -34,7 +34,7 @@
 // tokens below T.
 #include "internal.h"
 #include "common.cuh"
-#include "tmem.cuh"
+#include "mma.cuh"
 #include "tmap.h"
 
 namespace mb {
