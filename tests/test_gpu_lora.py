@@ -288,3 +288,12 @@ def test_first_products_above_the_largest_bf16(cuda_dev, T, bf16):
     got = eb.lora_add(i["base"], i["x"], i["a"], i["b"], i["adapter_ids"])
     torch.cuda.synchronize()
     assert bool(got.isfinite().all()) and bool(((got.double() - want).abs() <= tol).all())
+
+
+@pytest.mark.parametrize("T,bf16", [(30, False), (30, True), (500, False), (500, True)])
+def test_addresses_of_16_bytes_from_an_empty_output(cuda_dev, T, bf16):
+    """Every row is written, also those without an adapter: out holds NaN before the call."""
+    i = {k: _shifted(v) for k, v in _inputs(cuda_dev, T, 520, 264, 24, 3, bf16, seed=12).items()}
+    out = _shifted(torch.full_like(i["base"], float("nan")))
+    assert bool((i["adapter_ids"] < 0).any())
+    _check(i, out=out)
