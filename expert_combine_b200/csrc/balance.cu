@@ -34,8 +34,9 @@
 // their shared memory: one launch, no workspace.  Results do not depend on
 // timing.
 //
-// 65536 x 512, k = 22: loss 36 us (floor at the copy rate 21), gradient 72 us
-// (43); 32768 x 2560, k = 8: 82 us (51) and 132 us (103).
+// From a graph, 65536 x 512, k = 22: loss 36 us (floor at the copy rate 21),
+// gradient 73 us (43); 32768 x 2560, k = 8: 82 us (51) and 133 us (103; called
+// one by one 138).
 #include "internal.h"
 #include "common.cuh"
 
@@ -49,6 +50,7 @@ constexpr int kBalWarps = 24;                // most warps of a CTA (one CTA per
 constexpr int kBalGradWarps = 16;            // of the gradient, which needs twice the registers, and of a cluster's CTAs
 constexpr int kBalGateWarps = 4;             // warps of the gradient for the gate's own part
 static_assert(kBalGradWarps <= 4 * kBalGateWarps, "a gate warp serves four teams at most");
+static_assert(kBalWarps / 2 <= 15 && kBalGradWarps / 2 <= 15, "a team of several warps has a hardware barrier of its own, 1 .. 15");
 constexpr int kBalTags = 1024;               // marks per row for finding repeated picks
 constexpr int kBalLists = 4;                 // lists of entries a team has under way
 constexpr int kBalRowsPerTeam = 128;         // most rows a team adds up in one FP32 register
@@ -86,7 +88,6 @@ BalPlan bal_plan(int T, int E, int Q, bool grad) {
     p.cluster = !grad && T <= kBalCluster * (kBalGradWarps / p.W) * kBalClusterRows &&
                 static_cast<int64_t>(T) * E <= kBalClusterLogits && static_cast<int64_t>(Q) * E <= kBalClusterSums;
     p.teams = (grad || p.cluster ? kBalGradWarps : kBalWarps) / p.W;
-    if (p.W > 1 && p.teams > 15) p.teams = 15;      // a team of several warps has a hardware barrier of its own, 1 .. 15
     const int64_t ctas = p.cluster ? kBalCluster : kBalTargetCtas;
     // as many rows a team as fill the card's teams, in several waves where that were more than kBalRowsPerTeam
     const int64_t per = ctas * p.teams;
@@ -151,9 +152,9 @@ constexpr float kLog2e = 1.4426950408889634f;
 // The sigmoids of two logits, e their exponentials exp(-x).  One reciprocal
 // serves both, 1 / a = b / (a b): the special-function unit, which bounds these
 // kernels next to DRAM, forms 3 results for a pair instead of 4.  `big` grows
-// to infinity where a b leaves the range in which its reciprocal is normal (two
-// logits that add up to less than -87); the row is then done over by
-// sigmoid_over.
+// to infinity where a b leaves the range in which its reciprocal is normal (the
+// pair's logits, those above 0 taken for 0, add up to less than -87); the row
+// is then done over by sigmoid_over.
 __device__ __forceinline__ float2 sigmoid2(float2 x, float2& e, float& big) {
     const float2 t = mul2(x, make_float2(-kLog2e, -kLog2e));
     e = make_float2(ex2_approx(t.x), ex2_approx(t.y));
@@ -796,7 +797,7 @@ __device__ __forceinline__ void gate_lists(const BalArgs& a, int g, int t0, int 
 // that fall to its part of the row into a part-row of shared memory (zero
 // elsewhere) and adds that in the dense pass, so every logit's gradient is
 // written once, in full lines.  (With the gate in the teams themselves 32768 x
-// 2560 took 177 us instead of 131.)
+// 2560 took 177 us instead of 133.)
 template <int NV, bool VEC, bool BAL>
 __global__ void __launch_bounds__((kBalGradWarps + kBalGateWarps) * 32, 1) gate_grad_kernel(const BalArgs a) {
     constexpr int NE = 4 * NV;

@@ -41,8 +41,9 @@
 //     thread reads its row without bank conflicts, the sum replaces it there,
 //     and the warp writes whole 128-byte rows of out.
 // In steady state both move about 25 bytes a cycle and SM between L2 and the
-// SMs.  8192 tokens x 8192 -> 8192, rank 64, BF16: 95 us (x, base and out alone
-// are 61 at the copy rate); -> 256 columns, rank 32, FP32: 47 us.
+// SMs.  From a graph, 8192 tokens x 8192 -> 8192, rank 64, BF16: 94 us (x, base
+// and out alone are 61 at the copy rate; called one by one 96 to 101); -> 256
+// columns, rank 32, FP32: 47 us.
 #include "internal.h"
 #include "common.cuh"
 #include "tmap.h"
@@ -284,8 +285,9 @@ constexpr int kLmEpiWarps = 8;
 constexpr int kLmBytes = 208 * 1024;         // ring buffers of a CTA
 constexpr int kLmMaxStages = 12;
 // Fewest steps worth a CTA of the shrink: the CTA that adds a tile's partials
-// waits for each four of them (64 tokens of one adapter, rank 128, 8192 -> 256:
-// 30 us with 8 steps, 62 with 1; 8192 tokens: the same).
+// waits for each four of them (one adapter, rank 128, 8192 -> 256: 256 tokens
+// 33 us with 8 steps, 76 with 1; 512 tokens 33 and 57; 8192 tokens of four
+// adapters: the same).
 constexpr int kLmLeast = 8;
 constexpr int kLmChain = 4;                  // steps (of 2 slabs) the shrink adds up in tensor memory, see below
 constexpr unsigned int kLmTimeout = 32u;     // bit 5 of the device status word
