@@ -253,7 +253,9 @@ def device_status() -> int:
 def moe_route(logits: torch.Tensor, bias: torch.Tensor, token_mask: torch.Tensor, k: int,
               topk_ids: Optional[torch.Tensor] = None, topk_weights: Optional[torch.Tensor] = None,
               stream=None):
-    """Sigmoid router gate -> (topk_ids int32 [T, k], topk_weights float32 [T, k])."""
+    """Sigmoid router gate -> (topk_ids int32 [T, k], topk_weights float32 [T, k]).
+
+    Records no gradient; moe_route_backward forms the logits' from the weights'."""
     _want(logits, torch.float32, "logits")
     _want(bias, torch.float32, "bias")
     _want(token_mask, torch.uint8, "token_mask")

@@ -244,7 +244,8 @@ int expert_combine_join(const uint16_t* expert_out, int64_t num_rows, int H, con
  *   loss            = coeff / Q' * sum_q E / (k n_q^2)
  *                     * sum_e counts[q, e] * prob_sums[q, e]
  * over the Q' sequences that have a valid token (0 when none has).  A token
- * whose logits are all -inf adds nothing to prob_sums.  The probabilities are
+ * whose logits are all -inf adds nothing to prob_sums; NaN among them makes
+ * its sequence's prob_sums and the loss NaN.  The probabilities are
  * formed relative to the token's largest sigmoid, so logits far below zero
  * keep theirs.
  *
@@ -286,7 +287,8 @@ int moe_balance_loss(const float* logits, const int32_t* topk_ids, const uint8_t
  *     grad[t, e] += (g_e - sum_i g_i s_i / S) * s_e (1 - s_e) / S
  *     (the counts are constants)
  * The selection bias gets no gradient: it only selects.  Rows of invalid
- * tokens are zero.  counts, seq_tokens, seq_offsets, Q and coeff are those of
+ * tokens are zero, and rows of no sequence hold the gate's part alone, also
+ * where grad_loss is infinite or NaN.  counts, seq_tokens, seq_offsets, Q and coeff are those of
  * the moe_balance_loss call, and unused when grad_loss is NULL.
  *
  *   grad_weights [T, k] FP32 or NULL     grad_loss [1] FP32 on the device or NULL
