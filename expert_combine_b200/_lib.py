@@ -2,7 +2,7 @@
 from __future__ import annotations
 
 import ctypes
-import inspect
+import functools
 import os
 import threading
 from typing import Optional
@@ -37,36 +37,15 @@ def tracing() -> bool:
     return _trace_depth > 0
 
 
-def _beside(stream, fn, args, kwargs):
-    """A call on the caller's ``stream``, which is the current one meanwhile: what
-    the call allocates is then that stream's memory.  A block of the caller's
-    own current stream could still be in use there, and a workspace, dropped on
-    return, could be handed out there again while the kernels run.  The outputs
-    are marked as used on the caller's current stream too."""
-    if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(stream.cuda_stream)
-    before = torch.cuda.current_stream(stream.device)
-    with torch.cuda.stream(stream):
-        result = fn(*args, **kwargs)
-    if before != stream:
-        for t in result if isinstance(result, (tuple, list)) else (result,):
-            if isinstance(t, torch.Tensor):
-                t.record_stream(before)
-    return result
-
-
-def _entry(fn):
-    """A public call: its NVTX range, and its ``stream`` argument (the last)."""
+def _traced(fn):
     name = fn.__name__
-    place = list(inspect.signature(fn).parameters).index("stream")
 
     def wrapper(*args, **kwargs):
-        stream = kwargs.get("stream") if len(args) <= place else args[place]
         if _trace_depth <= 0:
-            return fn(*args, **kwargs) if stream is None else _beside(stream, fn, args, kwargs)
+            return fn(*args, **kwargs)
         torch.cuda.nvtx.range_push(name)
         try:
-            return fn(*args, **kwargs) if stream is None else _beside(stream, fn, args, kwargs)
+            return fn(*args, **kwargs)
         finally:
             torch.cuda.nvtx.range_pop()
 
@@ -75,7 +54,6 @@ def _entry(fn):
     wrapper.__doc__ = fn.__doc__
     wrapper.__wrapped__ = fn
     return wrapper
-
 
 STAGE_ROUTE = 0
 STAGE_NORM_QUANT = 1
@@ -196,6 +174,31 @@ def _stream(stream) -> ctypes.c_void_p:
     return ctypes.c_void_p(stream.cuda_stream)
 
 
+def _empty(stream):
+    """torch.empty for what a call's caller left out, of the memory of the stream
+    that the call runs on.  With another ``stream`` than the current one, a block
+    of the current stream's memory could still be in use there, and a workspace,
+    dropped on return, could be handed out there again while the kernels run."""
+    return torch.empty if stream is None else functools.partial(_empty_on, stream)
+
+
+def _empty_on(stream, *shape, dtype, device) -> torch.Tensor:
+    if stream.cuda_stream == _raw_stream(device.index):
+        return torch.empty(*shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream.cuda_stream, device)
+    here, before = torch.cuda.current_device(), torch.cuda.current_stream(device)
+    torch.cuda.set_stream(stream)        # and its device; takes half the time of the context manager
+    try:
+        t = torch.empty(*shape, dtype=dtype, device=device)
+    finally:
+        torch.cuda.set_stream(before)
+        if device.index != here:
+            torch.cuda.set_device(here)
+    t.record_stream(before)              # which the caller may use the result on
+    return t
+
+
 def _want(t: torch.Tensor, dtype: torch.dtype, name: str) -> None:
     if t.dtype != dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
@@ -249,7 +252,7 @@ def device_status() -> int:
     return v
 
 
-@_entry
+@_traced
 def moe_route(logits: torch.Tensor, bias: torch.Tensor, token_mask: torch.Tensor, k: int,
               topk_ids: Optional[torch.Tensor] = None, topk_weights: Optional[torch.Tensor] = None,
               stream=None):
@@ -260,10 +263,11 @@ def moe_route(logits: torch.Tensor, bias: torch.Tensor, token_mask: torch.Tensor
     _want(bias, torch.float32, "bias")
     _want(token_mask, torch.uint8, "token_mask")
     T, E = logits.shape
+    empty = _empty(stream)
     if topk_ids is None:
-        topk_ids = torch.empty(T, k, dtype=torch.int32, device=logits.device)
+        topk_ids = empty(T, k, dtype=torch.int32, device=logits.device)
     if topk_weights is None:
-        topk_weights = torch.empty(T, k, dtype=torch.float32, device=logits.device)
+        topk_weights = empty(T, k, dtype=torch.float32, device=logits.device)
     _want(topk_ids, torch.int32, "topk_ids")
     _want(topk_weights, torch.float32, "topk_weights")
     if bias.numel() != E or token_mask.numel() != T or topk_ids.shape != (T, k) \
@@ -274,12 +278,13 @@ def moe_route(logits: torch.Tensor, bias: torch.Tensor, token_mask: torch.Tensor
     return topk_ids, topk_weights
 
 
-@_entry
+@_traced
 def moe_route_check_fast_sigmoid(stream=None) -> float:
     """Largest |fast - exact| sigmoid over every binary32 input, measured on the
     device (the bound moe_route's shortlist relies on); synchronises."""
     dev = torch.device("cuda", torch.cuda.current_device())
-    out = torch.empty(1, dtype=torch.float32, device=dev)
+    empty = _empty(stream)
+    out = empty(1, dtype=torch.float32, device=dev)
     _check("moe_route_check_fast_sigmoid", load().moe_route_check_fast_sigmoid(_ptr(out), _stream(stream)))
     torch.cuda.synchronize(dev)
     return float(out.item())
@@ -289,7 +294,7 @@ def moe_route_check_fast_sigmoid(stream=None) -> float:
 ROUTE_FAST_SIGMOID_BOUND = 2.0 ** -21
 
 
-@_entry
+@_traced
 def norm_quant_nvfp4(x: torch.Tensor, num_tokens: int, norm_w: torch.Tensor, gain_center: float,
                      eps: float, global_scale: torch.Tensor, tp: int = 1,
                      packed: Optional[torch.Tensor] = None, sf: Optional[torch.Tensor] = None,
@@ -306,10 +311,11 @@ def norm_quant_nvfp4(x: torch.Tensor, num_tokens: int, norm_w: torch.Tensor, gai
     M = int(num_tokens)
     if x.numel() != M * H:
         raise ValueError("norm_quant_nvfp4: x must hold num_tokens * H elements")
+    empty = _empty(stream)
     if packed is None:
-        packed = torch.empty(M, H // 2, dtype=torch.uint8, device=x.device)
+        packed = empty(M, H // 2, dtype=torch.uint8, device=x.device)
     if sf is None:
-        sf = torch.empty(M, H // 16, dtype=torch.uint8, device=x.device)
+        sf = empty(M, H // 16, dtype=torch.uint8, device=x.device)
     _want(packed, torch.uint8, "packed")
     _want(sf, torch.uint8, "sf")
     if packed.numel() != M * (H // 2) or sf.numel() != M * (H // 16):
@@ -320,7 +326,7 @@ def norm_quant_nvfp4(x: torch.Tensor, num_tokens: int, norm_w: torch.Tensor, gai
     return packed, sf
 
 
-@_entry
+@_traced
 def moe_route_norm_quant(logits: torch.Tensor, bias: torch.Tensor, token_mask: torch.Tensor, k: int,
                          x: torch.Tensor, norm_w: torch.Tensor, gain_center: float, eps: float,
                          global_scale: torch.Tensor, tp: int = 1,
@@ -343,14 +349,15 @@ def moe_route_norm_quant(logits: torch.Tensor, bias: torch.Tensor, token_mask: t
     if x.numel() != T * H or bias.numel() != E or token_mask.numel() != T:
         raise ValueError("moe_route_norm_quant: shape mismatch")
     dev = logits.device
+    empty = _empty(stream)
     if topk_ids is None:
-        topk_ids = torch.empty(T, k, dtype=torch.int32, device=dev)
+        topk_ids = empty(T, k, dtype=torch.int32, device=dev)
     if topk_weights is None:
-        topk_weights = torch.empty(T, k, dtype=torch.float32, device=dev)
+        topk_weights = empty(T, k, dtype=torch.float32, device=dev)
     if packed is None:
-        packed = torch.empty(T, H // 2, dtype=torch.uint8, device=dev)
+        packed = empty(T, H // 2, dtype=torch.uint8, device=dev)
     if sf is None:
-        sf = torch.empty(T, H // 16, dtype=torch.uint8, device=dev)
+        sf = empty(T, H // 16, dtype=torch.uint8, device=dev)
     for t, dt, name in ((topk_ids, torch.int32, "topk_ids"), (topk_weights, torch.float32, "topk_weights"),
                         (packed, torch.uint8, "packed"), (sf, torch.uint8, "sf")):
         _want(t, dt, name)
@@ -368,7 +375,7 @@ def route_norm_quant_kernels(M: int, H: int, E: int, k: int, tp: int = 1) -> int
     device (for a 16-byte-aligned x); -1 when unsupported or without a device."""
     return int(load().moe_route_norm_quant_kernels(M, H, tp, E, k))
 
-@_entry
+@_traced
 def expert_combine(expert_out: torch.Tensor, num_rows: int, row_idx: torch.Tensor,
                    weights: torch.Tensor, norm_w: torch.Tensor, gain_center: float, eps: float,
                    out: Optional[torch.Tensor] = None, stream=None):
@@ -381,8 +388,9 @@ def expert_combine(expert_out: torch.Tensor, num_rows: int, row_idx: torch.Tenso
     T, k = row_idx.shape
     if weights.shape != (T, k) or expert_out.shape[-1] != H:
         raise ValueError("expert_combine: shape mismatch")
+    empty = _empty(stream)
     if out is None:
-        out = torch.empty(T, H, dtype=torch.bfloat16, device=row_idx.device)
+        out = empty(T, H, dtype=torch.bfloat16, device=row_idx.device)
     _want(out, torch.bfloat16, "out")
     _check("expert_combine",
            load().expert_combine(_ptr(expert_out), int(num_rows), H, _ptr(row_idx), _ptr(weights),
@@ -391,7 +399,7 @@ def expert_combine(expert_out: torch.Tensor, num_rows: int, row_idx: torch.Tenso
     return out
 
 
-@_entry
+@_traced
 def residual_join(residual: torch.Tensor, branch: torch.Tensor, gain: torch.Tensor, alpha: float,
                   beta: float, eps: float, next_w: Optional[torch.Tensor] = None,
                   next_gc: float = 1.0, next_eps: float = 1e-6,
@@ -403,10 +411,11 @@ def residual_join(residual: torch.Tensor, branch: torch.Tensor, gain: torch.Tens
     T, H = residual.shape
     if branch.shape != (T, H) or gain.numel() != H:
         raise ValueError("residual_join: shape mismatch")
+    empty = _empty(stream)
     if next_w is not None:
         _want(next_w, torch.bfloat16, "next_w")
         if next_prenorm is None:
-            next_prenorm = torch.empty(T, H, dtype=torch.bfloat16, device=residual.device)
+            next_prenorm = empty(T, H, dtype=torch.bfloat16, device=residual.device)
         _want(next_prenorm, torch.bfloat16, "next_prenorm")
     _check("residual_join",
            load().residual_join(_ptr(residual), _ptr(branch), _ptr(gain), float(alpha),
@@ -415,7 +424,7 @@ def residual_join(residual: torch.Tensor, branch: torch.Tensor, gain: torch.Tens
     return next_prenorm
 
 
-@_entry
+@_traced
 def expert_combine_join(expert_out: torch.Tensor, num_rows: int, row_idx: torch.Tensor,
                         weights: torch.Tensor, norm_w: torch.Tensor, gain_center: float,
                         eps: float, residual: torch.Tensor, gain: torch.Tensor, alpha: float,
@@ -436,10 +445,11 @@ def expert_combine_join(expert_out: torch.Tensor, num_rows: int, row_idx: torch.
         raise ValueError("expert_combine_join: shape mismatch")
     if out is not None:
         _want(out, torch.bfloat16, "out")
+    empty = _empty(stream)
     if next_w is not None:
         _want(next_w, torch.bfloat16, "next_w")
         if next_prenorm is None:
-            next_prenorm = torch.empty(T, H, dtype=torch.bfloat16, device=residual.device)
+            next_prenorm = empty(T, H, dtype=torch.bfloat16, device=residual.device)
     _check("expert_combine_join",
            load().expert_combine_join(_ptr(expert_out), int(num_rows), H, _ptr(row_idx),
                                       _ptr(weights), T, k, _ptr(norm_w), float(gain_center),
@@ -455,7 +465,7 @@ def dispatch_workspace_size(T: int, k: int, E: int) -> int:
     return int(load().moe_dispatch_workspace_size(T, k, E))
 
 
-@_entry
+@_traced
 def moe_dispatch(topk_ids: torch.Tensor, num_experts: int, expert_begin: int = 0,
                  expert_offsets: Optional[torch.Tensor] = None, row_idx: Optional[torch.Tensor] = None,
                  row_token: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
@@ -470,12 +480,13 @@ def moe_dispatch(topk_ids: torch.Tensor, num_experts: int, expert_begin: int = 0
     T, k = topk_ids.shape
     E = int(num_experts)
     dev = topk_ids.device
+    empty = _empty(stream)
     if expert_offsets is None:
-        expert_offsets = torch.empty(E + 1, dtype=torch.int32, device=dev)
+        expert_offsets = empty(E + 1, dtype=torch.int32, device=dev)
     if row_idx is None:
-        row_idx = torch.empty(T, k, dtype=torch.int32, device=dev)
+        row_idx = empty(T, k, dtype=torch.int32, device=dev)
     if row_token is None:
-        row_token = torch.empty(T * k, dtype=torch.int32, device=dev)
+        row_token = empty(T * k, dtype=torch.int32, device=dev)
     _want(expert_offsets, torch.int32, "expert_offsets")
     _want(row_idx, torch.int32, "row_idx")
     _want(row_token, torch.int32, "row_token")
@@ -483,7 +494,7 @@ def moe_dispatch(topk_ids: torch.Tensor, num_experts: int, expert_begin: int = 0
         raise ValueError("moe_dispatch: shape mismatch")
     need = dispatch_workspace_size(T, k, E)
     if workspace is None and need > 0:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        workspace = empty(need, dtype=torch.uint8, device=dev)
     if workspace is not None:
         _want(workspace, torch.uint8, "workspace")
     ws_bytes = 0 if workspace is None else workspace.numel()
@@ -493,7 +504,7 @@ def moe_dispatch(topk_ids: torch.Tensor, num_experts: int, expert_begin: int = 0
     return expert_offsets, row_idx, row_token
 
 
-@_entry
+@_traced
 def moe_dispatch_noalloc(topk_ids: torch.Tensor, num_experts: int, expert_begin: int = 0,
                          expert_offsets: Optional[torch.Tensor] = None,
                          row_idx: Optional[torch.Tensor] = None,
@@ -508,12 +519,13 @@ def moe_dispatch_noalloc(topk_ids: torch.Tensor, num_experts: int, expert_begin:
     T, k = topk_ids.shape
     E = int(num_experts)
     dev = topk_ids.device
+    empty = _empty(stream)
     if expert_offsets is None:
-        expert_offsets = torch.empty(E + 1, dtype=torch.int32, device=dev)
+        expert_offsets = empty(E + 1, dtype=torch.int32, device=dev)
     if row_idx is None:
-        row_idx = torch.empty(T, k, dtype=torch.int32, device=dev)
+        row_idx = empty(T, k, dtype=torch.int32, device=dev)
     if row_token is None:
-        row_token = torch.empty(T * k, dtype=torch.int32, device=dev)
+        row_token = empty(T * k, dtype=torch.int32, device=dev)
     _want(expert_offsets, torch.int32, "expert_offsets")
     _want(row_idx, torch.int32, "row_idx")
     _want(row_token, torch.int32, "row_token")
@@ -544,7 +556,7 @@ def _router_batch(fn, logits, topk_ids, token_mask, seq_offsets):
     return T, E, k, Q, dev, at
 
 
-@_entry
+@_traced
 def moe_balance_loss(logits: torch.Tensor, topk_ids: torch.Tensor, token_mask: torch.Tensor, coeff: float,
                      seq_offsets: Optional[torch.Tensor] = None, loss: Optional[torch.Tensor] = None,
                      counts: Optional[torch.Tensor] = None, prob_sums: Optional[torch.Tensor] = None,
@@ -568,24 +580,25 @@ def moe_balance_loss(logits: torch.Tensor, topk_ids: torch.Tensor, token_mask: t
     T, E, k, Q, dev, (at_logits, at_ids, at_mask, at_offsets) = _router_batch(fn, logits, topk_ids, token_mask,
                                                                               seq_offsets)
     where = logits.device
+    empty = _empty(stream)
     if loss is None:
-        loss = torch.empty(1, dtype=torch.float32, device=where)
+        loss = empty(1, dtype=torch.float32, device=where)
     if counts is None:
-        counts = torch.empty(Q, E, dtype=torch.int32, device=where)
+        counts = empty(Q, E, dtype=torch.int32, device=where)
     elif counts.shape != (Q, E):
         raise ValueError(f"{fn}: shape mismatch")
     if prob_sums is None:
-        prob_sums = torch.empty(Q, E, dtype=torch.float32, device=where)
+        prob_sums = empty(Q, E, dtype=torch.float32, device=where)
     elif prob_sums.shape != (Q, E):
         raise ValueError(f"{fn}: shape mismatch")
     if seq_tokens is None:
-        seq_tokens = torch.empty(Q, dtype=torch.int32, device=where)
+        seq_tokens = empty(Q, dtype=torch.int32, device=where)
     if loss.numel() != 1 or seq_tokens.numel() != Q:
         raise ValueError(f"{fn}: shape mismatch")
     if workspace is None:
         need = load().moe_balance_workspace_size(T, E, Q)
         if need > 0:
-            workspace = torch.empty(need, dtype=torch.uint8, device=where)
+            workspace = empty(need, dtype=torch.uint8, device=where)
     _enqueue(fn, dev, stream, at_logits, at_ids, at_mask, T, E, k, at_offsets, Q, coeff,
              _take(loss, torch.float32, dev, "loss"), _take(counts, torch.int32, dev, "counts"),
              _take(prob_sums, torch.float32, dev, "prob_sums"), _take(seq_tokens, torch.int32, dev, "seq_tokens"),
@@ -593,7 +606,7 @@ def moe_balance_loss(logits: torch.Tensor, topk_ids: torch.Tensor, token_mask: t
     return loss, counts, prob_sums, seq_tokens
 
 
-@_entry
+@_traced
 def moe_route_backward(logits: torch.Tensor, topk_ids: torch.Tensor, token_mask: torch.Tensor,
                        grad_weights: Optional[torch.Tensor] = None, grad_loss: Optional[torch.Tensor] = None,
                        coeff: Optional[float] = None, counts: Optional[torch.Tensor] = None,
@@ -614,7 +627,8 @@ def moe_route_backward(logits: torch.Tensor, topk_ids: torch.Tensor, token_mask:
         if grad_loss.numel() != 1 or counts.shape != (Q, E) or seq_tokens.numel() != Q:
             raise ValueError(f"{fn}: shape mismatch")
     if grad_logits is None:
-        grad_logits = torch.empty_like(logits)
+        grad_logits = torch.empty_like(logits) if stream is None else \
+            _empty_on(stream, T, E, dtype=torch.float32, device=logits.device)
     elif grad_logits.shape != (T, E):
         raise ValueError(f"{fn}: shape mismatch")
     _enqueue(fn, dev, stream, at_logits, at_ids, at_mask, T, E, k,
@@ -625,13 +639,14 @@ def moe_route_backward(logits: torch.Tensor, topk_ids: torch.Tensor, token_mask:
     return grad_logits
 
 
-@_entry
+@_traced
 def router_weight_prepare(w: torch.Tensor, w3: Optional[torch.Tensor] = None, stream=None):
     """FP32 router weight [E, H] -> its three BF16 parts [3, E, H] (done once)."""
     _want(w, torch.float32, "w")
     E, H = w.shape
+    empty = _empty(stream)
     if w3 is None:
-        w3 = torch.empty(3, E, H, dtype=torch.bfloat16, device=w.device)
+        w3 = empty(3, E, H, dtype=torch.bfloat16, device=w.device)
     _want(w3, torch.bfloat16, "w3")
     if w3.shape != (3, E, H):
         raise ValueError("router_weight_prepare: shape mismatch")
@@ -639,7 +654,7 @@ def router_weight_prepare(w: torch.Tensor, w3: Optional[torch.Tensor] = None, st
     return w3
 
 
-@_entry
+@_traced
 def router_logits(x: torch.Tensor, w3: torch.Tensor, scale: float = 1.0,
                   logits: Optional[torch.Tensor] = None, stream=None):
     """Router projection on the tensor cores: logits float32 [T, E] =
@@ -650,8 +665,9 @@ def router_logits(x: torch.Tensor, w3: torch.Tensor, scale: float = 1.0,
     E = w3.shape[1]
     if w3.shape != (3, E, H):
         raise ValueError("router_logits: shape mismatch")
+    empty = _empty(stream)
     if logits is None:
-        logits = torch.empty(T, E, dtype=torch.float32, device=x.device)
+        logits = empty(T, E, dtype=torch.float32, device=x.device)
     _want(logits, torch.float32, "logits")
     if logits.shape != (T, E):
         raise ValueError("router_logits: shape mismatch")
@@ -665,7 +681,7 @@ def lora_workspace_size(T: int, H: int, N: int, R: int, L: int) -> int:
     return int(load().lora_workspace_size(T, H, N, R, L))
 
 
-@_entry
+@_traced
 def lora_add(base: torch.Tensor, x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, adapter_ids: torch.Tensor,
              scales: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
              workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
@@ -689,13 +705,13 @@ def lora_add(base: torch.Tensor, x: torch.Tensor, a: torch.Tensor, b: torch.Tens
             scales is not None and scales.numel() != L):
         raise ValueError(f"{fn}: shape mismatch")
     if out is None:
-        out = torch.empty_like(base)
+        out = torch.empty_like(base) if stream is None else _empty_on(stream, T, N, dtype=dtype, device=base.device)
     elif out.shape != base.shape:
         raise ValueError(f"{fn}: shape mismatch")
     if workspace is None:
         need = load().lora_workspace_size(T, H, N, R, L)
         if need > 0:
-            workspace = torch.empty(need, dtype=torch.uint8, device=base.device)
+            workspace = _empty(stream)(need, dtype=torch.uint8, device=base.device)
     _enqueue(fn, dev, stream, _take(base, dtype, dev, "base"), bf16, _take(x, torch.bfloat16, dev, "x"), T, H,
              _take(a, torch.bfloat16, dev, "a"), _take(b, torch.bfloat16, dev, "b"), N, R, L,
              _take(adapter_ids, torch.int32, dev, "adapter_ids"), _take(scales, torch.float32, dev, "scales"),
@@ -710,7 +726,7 @@ def finalize_ar_workspace_size(world: int, T_max: int, H: int) -> int:
     return int(load().finalize_ar_workspace_size(world, T_max, H))
 
 
-@_entry
+@_traced
 def finalize_ar_workspace_init(workspace, world: int, T_max: int, H: int, stream=None) -> None:
     """Zero a workspace's call counter and flags (a tensor or a device address)."""
     ptr = _ptr(workspace) if isinstance(workspace, torch.Tensor) else ctypes.c_void_p(int(workspace))
@@ -733,7 +749,7 @@ def _far_rank_check(fn, expert_out, row_idx, weights, norm_w, out):
         raise ValueError(f"{fn}: shape mismatch")
 
 
-@_entry
+@_traced
 def expert_finalize_allreduce(expert_out: torch.Tensor, num_rows: int, row_idx: torch.Tensor,
                               weights: torch.Tensor, norm_w: torch.Tensor, gain_center: float, eps: float,
                               workspaces, rank: int, T_max: int, out: Optional[torch.Tensor] = None,
@@ -747,8 +763,9 @@ def expert_finalize_allreduce(expert_out: torch.Tensor, num_rows: int, row_idx: 
     _want(norm_w, torch.bfloat16, "norm_w")
     T, k = row_idx.shape
     H = norm_w.numel()
+    empty = _empty(stream)
     if out is None:
-        out = torch.empty(T, H, dtype=torch.bfloat16, device=row_idx.device)
+        out = empty(T, H, dtype=torch.bfloat16, device=row_idx.device)
     _far_rank_check("expert_finalize_allreduce", expert_out, row_idx, weights, norm_w, out)
     world = len(workspaces)
     ws = (ctypes.c_void_p * world)(*[_addr(w) for w in workspaces])
@@ -760,7 +777,7 @@ def expert_finalize_allreduce(expert_out: torch.Tensor, num_rows: int, row_idx: 
     return out
 
 
-@_entry
+@_traced
 def expert_finalize_allreduce_local(expert_outs, num_rows, row_idx, weights, norm_w: torch.Tensor,
                                     gain_center: float, eps: float, workspaces, T_max: int, outs=None,
                                     stream=None):
@@ -772,8 +789,9 @@ def expert_finalize_allreduce_local(expert_outs, num_rows, row_idx, weights, nor
         raise ValueError("expert_finalize_allreduce_local: one entry per rank in every list")
     T, k = row_idx[0].shape
     H = norm_w.numel()
+    empty = _empty(stream)
     if outs is None:
-        outs = [torch.empty(T, H, dtype=torch.bfloat16, device=norm_w.device) for _ in range(world)]
+        outs = [empty(T, H, dtype=torch.bfloat16, device=norm_w.device) for _ in range(world)]
     for r in range(world):
         if row_idx[r].shape != (T, k):
             raise ValueError("expert_finalize_allreduce_local: every rank's row_idx must be [T, k]")

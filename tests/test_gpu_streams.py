@@ -90,3 +90,18 @@ def test_stream_as_a_positional_argument(cuda_dev):
     w3 = eb.router_weight_prepare(x, None, side)
     torch.cuda.synchronize()
     assert torch.equal(got, want) and torch.equal(w3, eb.router_weight_prepare(x))
+
+
+def test_the_current_stream_and_device_come_back(cuda_dev):
+    """Also after a refused call; outputs that the caller gave are the ones returned."""
+    x = torch.randn(16, 64, device=cuda_dev)
+    w3 = torch.empty(3, 16, 64, dtype=torch.bfloat16, device=cuda_dev)
+    before, side = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(before):
+        assert eb.router_weight_prepare(x, w3, stream=side) is w3
+        assert torch.cuda.current_stream() == before and torch.cuda.current_device() == cuda_dev.index
+        with pytest.raises(ValueError, match="contiguous"):
+            eb.router_weight_prepare(x.t(), stream=side)
+        assert torch.cuda.current_stream() == before and torch.cuda.current_device() == cuda_dev.index
+    torch.cuda.synchronize()
